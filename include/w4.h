@@ -429,6 +429,121 @@ w4_status w4_gemv_batched(int32_t codec, int32_t m, int32_t y_dtype,
                           w4_gemv_problem* problems_device, const w4_gemv_batch_info* info,
                           void* stream);
 
+/*
+ * ---- MX (microscaled) operators -------------------------------------------
+ * Weights in the OCP microscaling 4-bit floating-point form, multiplied as
+ * stored by activations in the same 4-bit or an 8-bit form: the matrix core
+ * takes elements and scales directly, nothing is rebuilt.  w4_mx_rmsnorm and
+ * w4_mx_quantize make the activations; w4_mx_linear and w4_mx_grouped_linear
+ * (mixture-of-experts layers) multiply.  The conventions at the top of this
+ * header hold, except that non-finite values are defined here.
+ *
+ * An MX tensor [rows][k], k a multiple of 32, is two planar row-major arrays:
+ *   elements  W4_MXFP4: uint8 [rows][k/2], element c in the low (c even) or
+ *             high nibble of byte c/2: sign << 3 | index of {0, 0.5, 1, 1.5,
+ *             2, 3, 4, 6};
+ *             W4_MXFP8: uint8 [rows][k], E4M3 (bias 7, largest 448, 0x7F and
+ *             0xFF NaN, no infinities);
+ *   scales    uint8 [rows][k/32]: byte b of 32 consecutive values along k
+ *             stands for 2^(b - 127); 255 makes the whole block NaN.
+ * value = element * 2^(b - 127).
+ */
+typedef enum { W4_MXFP4 = 0, W4_MXFP8 = 1 } w4_mx_format;
+
+/* Largest number of experts of a grouped product. */
+#define W4_MX_MAX_EXPERTS 4096
+
+/*
+ * w4_mx_quantize -- quantize x [rows][k] of x_dtype (W4_F32, W4_BF16 or W4_F16).
+ * Per block of 32, with a = max |x| and emax = 2 (W4_MXFP4) or 8 (W4_MXFP8):
+ *   b = clamp(floor(log2 a) - emax + 127, 0, 254), 0 where a = 0;
+ *   element = x * 2^(127 - b) rounded to the nearest element, ties to the even
+ *   code, magnitudes above the largest element becoming it; the sign of zero
+ *   is kept.
+ * A block with a NaN or an infinity gets b = 255 and zero elements.
+ * x, elements and scales 16-byte aligned.  rows == 0 or k == 0: nothing to do.
+ * Errors: W4_EINVAL (bad format, negative size, null pointer), W4_ESHAPE
+ * (k % 32 != 0, or more than 2^31 - 1 blocks of 2048 values), W4_EALIGN,
+ * W4_EUNSUPPORTED (x_dtype).
+ */
+w4_status w4_mx_quantize(int32_t format, int64_t rows, int64_t k, const void* x, int32_t x_dtype,
+                         uint8_t* elements, uint8_t* scales, void* stream);
+
+/*
+ * w4_mx_dequant -- the values of an MX tensor as out [rows][k] of out_dtype
+ * W4_BF16 or W4_F32.  Exact in fp32 (values of 2^128 and more become infinite);
+ * bf16 rounds to nearest even, which only changes values below 2^-126.
+ * Alignment and errors as w4_mx_quantize.
+ */
+w4_status w4_mx_dequant(int32_t format, int64_t rows, int64_t k, const uint8_t* elements,
+                        const uint8_t* scales, void* out, int32_t out_dtype, void* stream);
+
+/*
+ * w4_mx_rmsnorm -- root-mean-square norm of each row, with the residual's
+ * addition before it and the MX form as its output.  With T the type `dtype`
+ * (W4_F32, W4_BF16, W4_F16) of x, residual, gamma, residual_out and y:
+ *   h = x + residual in fp32, rounded to T (RNE) and written to residual_out
+ *       (residual == NULL: h = x, residual_out is not used);
+ *   v = h * gamma / sqrt(sum_c h^2 / k + eps) in fp32 (the row's factor is
+ *       computed in fp64 from fp32 partial sums);
+ *   y = RNE_T(v) unless y is NULL; elements, scales = w4_mx_quantize(v) unless
+ *       elements is NULL.  One of the two must be given.
+ * The sums are the same bits for the same shape.  A NaN or an infinity in a row
+ * of h makes the row's v NaN as IEEE arithmetic does, and so its blocks.
+ * residual_out may be the same buffer as residual or x; y likewise as x or
+ * residual when residual_out is another one.
+ * x, residual, residual_out, y [rows][k]; gamma [k].  All 16-byte aligned.
+ * Errors: W4_EINVAL (bad format, negative size, null pointer, eps negative or
+ * not finite), W4_ESHAPE (k % 32 != 0, rows above 2^31 - 1), W4_EALIGN,
+ * W4_EUNSUPPORTED (dtype).
+ */
+w4_status w4_mx_rmsnorm(int32_t format, int64_t rows, int64_t k, const void* x,
+                        const void* residual, const void* gamma, int32_t dtype, float eps,
+                        void* residual_out, void* y, uint8_t* elements, uint8_t* scales,
+                        void* stream);
+
+/*
+ * w4_mx_linear -- y[i][r] = sum_c X[i][c] W[r][c], W an MXFP4 weight [n][k], X
+ * [m][k] of x_format, fp32 accumulation, y of y_dtype W4_F32 (4-byte aligned)
+ * or W4_BF16 (RNE, 2-byte aligned).  Any m >= 0.  With W4_MXFP4 activations the
+ * products add exactly up to the fp32 accumulator's roundings; with W4_MXFP8
+ * the matrix core drops what lies about 2^-14 below the largest of a few
+ * neighbouring products (4e-6 of the result, measured in the 2-norm on normal
+ * data).  Both stay within the GEMV tolerance, 1e-3 * sum_c |X W| + 1e-6 (bf16
+ * y: plus 2^-8 |y|).  k == 0 (with m, n > 0): y = +0.  NaN blocks and elements
+ * make their row's (column's) results NaN.
+ * w, w_scales, x, x_scales 16-byte aligned.
+ * Errors: W4_EINVAL (bad format, negative size, null pointer), W4_ESHAPE
+ * (k % 32 != 0, k above W4_MAX_MATMUL_K, m above 2^31 - 1, too many tiles),
+ * W4_EALIGN, W4_EUNSUPPORTED (y_dtype).
+ */
+w4_status w4_mx_linear(int32_t x_format, int64_t n, int64_t k, const uint8_t* w,
+                       const uint8_t* w_scales, const uint8_t* x, const uint8_t* x_scales,
+                       int64_t m, void* y, int32_t y_dtype, void* stream);
+
+/*
+ * w4_mx_grouped_linear -- the products of many weights with ragged groups of
+ * rows, as in a mixture-of-experts layer: rows offsets[e] .. offsets[e+1] - 1
+ * of y [rows][n] use weight e of w (MXFP4 [experts][n][k]).  Row t of y takes
+ * row row_index[t] of x (x_format, [tokens][k]), or row t where row_index is
+ * NULL (tokens >= rows then).
+ * offsets: DEVICE int32 [experts + 1], not decreasing, offsets[0] = 0 (read as
+ * 0 whatever it holds); the host does not read it, so the groups can change
+ * between replays of a captured graph.  Rows from offsets[experts] on, which
+ * no expert has, are written as zeros: y may have room to spare.  Rows whose
+ * row_index lies outside [0, tokens) are zeros as well.  Offsets that decrease
+ * or pass `rows` are read as the nearest value that does not.
+ * Accumulation, y_dtype, tolerance, alignment (offsets and row_index 4 bytes)
+ * and errors as w4_mx_linear; also W4_ESHAPE for experts above
+ * W4_MX_MAX_EXPERTS or tokens below rows without row_index.  experts == 0: y is
+ * zeros.
+ */
+w4_status w4_mx_grouped_linear(int32_t x_format, int32_t experts, int64_t n, int64_t k,
+                               const uint8_t* w, const uint8_t* w_scales, int64_t tokens,
+                               const uint8_t* x, const uint8_t* x_scales, int64_t rows,
+                               const int32_t* offsets, const int32_t* row_index, void* y,
+                               int32_t y_dtype, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

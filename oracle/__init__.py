@@ -35,6 +35,8 @@ Modules
 ``dyadic5``   dyadic codes of 3, 4 or 5 bits per group in one 5-bit index space.
 ``warmstart`` the SIGNMAG8 warm start: 112 parametric transforms per group,
               the best one's 8 levels, then Lloyd rounds.
+``mx``        microscaled blocks (E2M1 / E4M3 elements): quantize, rebuild, RMS
+              norm, linear and grouped linear.
 ``matmul``    fp64 GEMV/GEMM on dequantized weights and the error bound.
 ``native``    ctypes loader for ``liboracle.so`` (plain C, same definitions,
               used where the Python loops would take minutes).
@@ -43,6 +45,7 @@ Functions that have no independent pin say "parity unpinned" in their
 docstring; every other function is pinned by ``tests/test_oracle_*.py``.
 """
 
-from . import bits, packing, dyadic, dyadic5, lut16, signmag8, warmstart, matmul  # noqa: F401
+from . import bits, packing, dyadic, dyadic5, lut16, signmag8, warmstart, matmul, mx  # noqa: F401
 
-__all__ = ["bits", "packing", "dyadic", "dyadic5", "lut16", "signmag8", "warmstart", "matmul"]
+__all__ = ["bits", "packing", "dyadic", "dyadic5", "lut16", "signmag8", "warmstart", "matmul",
+           "mx"]

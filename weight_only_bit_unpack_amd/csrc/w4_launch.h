@@ -75,4 +75,30 @@ size_t gemm_workspace_bytes(int codec, int64_t n, int64_t k, int m);
 hipError_t noalloc_scratch(char** out);
 constexpr size_t kNoallocScratchBytes = size_t{64} << 20;
 
+// ---- MX (microscaled) operators
+// One product y[m][n] = x w^T, or with offsets != nullptr the products of
+// `experts` weights with the rows of y that offsets gives each of them.
+struct MxProblem {
+  const uint8_t* w;         // fp4 elements [experts][n][k/2]
+  const uint8_t* w_scales;  // [experts][n][k/32]
+  const uint8_t* x;         // elements [tokens][k or k/2]
+  const uint8_t* x_scales;  // [tokens][k/32]
+  const int32_t* offsets;   // [experts + 1], or nullptr
+  const int32_t* row_index; // [m] rows of x, or nullptr: row i of y takes row i of x
+  void* y;                  // [m][n]
+  int64_t m, n, k, tokens;
+  int32_t experts, y_bf16;
+};
+
+hipError_t launch_mx_quantize(int fmt, int64_t rows, int64_t k, const void* x, int dtype, uint8_t* q,
+                              uint8_t* scales, hipStream_t stream);
+hipError_t launch_mx_dequant(int fmt, int64_t rows, int64_t k, const uint8_t* q, const uint8_t* scales,
+                             void* out, int dtype, hipStream_t stream);
+hipError_t launch_mx_rmsnorm(int fmt, int64_t rows, int64_t k, const void* x, const void* residual,
+                             const void* gamma, int dtype, float eps, void* residual_out, void* y,
+                             uint8_t* q, uint8_t* scales, hipStream_t stream);
+// blocks of the product's launch (at most 2^31 - 1 are possible)
+int64_t mx_linear_blocks(const MxProblem& p);
+hipError_t launch_mx_linear(int x_fmt, const MxProblem& p, hipStream_t stream);
+
 }  // namespace w4
