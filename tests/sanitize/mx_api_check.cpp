@@ -32,7 +32,7 @@ hipError_t launch_mx_rmsnorm(int, int64_t, int64_t, const void*, const void*, co
   ++g_launches;
   return hipSuccess;
 }
-int64_t mx_linear_blocks(const MxProblem&) { return g_blocks; }
+int64_t mx_linear_blocks(int, const MxProblem&) { return g_blocks; }
 hipError_t launch_mx_linear(int, const MxProblem& p, hipStream_t) {
   if (g_throw) throw std::bad_alloc();
   ++g_launches;

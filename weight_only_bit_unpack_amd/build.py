@@ -22,7 +22,7 @@ ARCH = "gfx950"
 
 SOURCES = ["w4_api.cpp", "w4_quantize.hip", "w4_dequant.hip", "w4_gemv.hip", "w4_gemm.hip",
            "w4_workspace.cpp", "w4_fit.hip", "w4_noalloc.hip", "w4_mx_api.cpp", "w4_mx_quant.hip",
-           "w4_mx_gemm.hip"]
+           "w4_mx_gemm.hip", "w4_mx_skinny.hip"]
 
 CFLAGS = [
     f"--offload-arch={ARCH}",

@@ -98,7 +98,10 @@ hipError_t launch_mx_rmsnorm(int fmt, int64_t rows, int64_t k, const void* x, co
                              const void* gamma, int dtype, float eps, void* residual_out, void* y,
                              uint8_t* q, uint8_t* scales, hipStream_t stream);
 // blocks of the product's launch (at most 2^31 - 1 are possible)
-int64_t mx_linear_blocks(const MxProblem& p);
+int64_t mx_linear_blocks(int x_fmt, const MxProblem& p);
 hipError_t launch_mx_linear(int x_fmt, const MxProblem& p, hipStream_t stream);
+// few rows of x a weight (w4_mx_skinny.hip)
+int64_t mx_skinny_blocks(int x_fmt, const MxProblem& p);
+hipError_t launch_mx_skinny(int x_fmt, const MxProblem& p, hipStream_t stream);
 
 }  // namespace w4

@@ -124,7 +124,7 @@ w4_status w4_mx_linear(int32_t x_format, int64_t n, int64_t k, const uint8_t* w,
   }
   const w4::MxProblem p{w, w_scales, x, x_scales, nullptr, nullptr, y, m, n, k, m, 1,
                         y_dtype == W4_BF16};
-  if (w4::mx_linear_blocks(p) > kMaxBlocks) return W4_ESHAPE;
+  if (w4::mx_linear_blocks(x_format, p) > kMaxBlocks) return W4_ESHAPE;
   return guarded([&] {
     const hipStream_t s = static_cast<hipStream_t>(stream);
     return k == 0 ? w4::launch_zero(y, m * n, y_dtype == W4_BF16, s)  // the empty sum
@@ -155,7 +155,7 @@ w4_status w4_mx_grouped_linear(int32_t x_format, int32_t experts, int64_t n, int
   }
   const w4::MxProblem p{w, w_scales, x, x_scales, offsets, row_index, y, rows, n, k, tokens,
                         experts, y_dtype == W4_BF16};
-  if (!none && w4::mx_linear_blocks(p) > kMaxBlocks) return W4_ESHAPE;
+  if (!none && w4::mx_linear_blocks(x_format, p) > kMaxBlocks) return W4_ESHAPE;
   return guarded([&] {
     const hipStream_t s = static_cast<hipStream_t>(stream);
     return none ? w4::launch_zero(y, rows * n, y_dtype == W4_BF16, s)

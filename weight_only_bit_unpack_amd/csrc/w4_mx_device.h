@@ -172,6 +172,77 @@ __device__ __forceinline__ void store8(void* x, int64_t g, const Raw8<DT>& r) {
   }
 }
 
+// Orders one lane's LDS accesses with another lane's of the same wave.  The
+// hardware runs a wave's LDS instructions in order; this keeps the compiler
+// from taking a value that this lane has not written to be the one it read
+// before.
+__device__ __forceinline__ void wave_lds_sync() {
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront", "local");
+  __builtin_amdgcn_wave_barrier();
+  __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "wavefront", "local");
+}
+
+// Buffer resource over `bytes` from base: loads at an offset past it return zero.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t mx_rsrc(const void* base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<void*>(base), (short)0, (int)bytes,
+                                           0x00020000);
+}
+// An offset past every resource (a block's rows hold at most 2^31 bytes).
+constexpr uint32_t kMxOOB = 0xFFFFFF00u;
+
+__device__ __forceinline__ u32x4 mx_load16(__amdgpu_buffer_rsrc_t r, uint32_t offset) {
+  const auto v = __builtin_amdgcn_raw_buffer_load_b128(r, offset, 0, 0);
+  return (u32x4){v[0], v[1], v[2], v[3]};
+}
+__device__ __forceinline__ uint32_t mx_load1(__amdgpu_buffer_rsrc_t r, uint32_t offset) {
+  return (uint32_t)__builtin_amdgcn_raw_buffer_load_b8(r, offset, 0, 0);
+}
+
+// Matrix operand registers: fp4 takes the first 16 bytes, fp8 both.
+template <int FMT>
+__device__ __forceinline__ i32x8 mx_operand(const u32x4& a, const u32x4& b) {
+  if constexpr (FMT == kMxFp4)
+    return (i32x8){(int)a.x, (int)a.y, (int)a.z, (int)a.w, 0, 0, 0, 0};
+  else
+    return (i32x8){(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+}
+
+// Four consecutive outputs of one row from column c on, where c + i < n.
+__device__ __forceinline__ void mx_store4(void* y, int y_bf16, int64_t row_base, int64_t c, int64_t n,
+                                          const f32x4& v) {
+  if (y_bf16) {
+    uint16_t* const p = reinterpret_cast<uint16_t*>(y) + row_base + c;
+    if (c + 4 <= n && (reinterpret_cast<uintptr_t>(p) & 7) == 0) {
+      *reinterpret_cast<u32x2*>(p) = (u32x2){cvt_pk_bf16(v.x, v.y), cvt_pk_bf16(v.z, v.w)};
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i < n) p[i] = (uint16_t)f32_to_bf16_bits(v[i]);
+    }
+  } else {
+    float* const p = reinterpret_cast<float*>(y) + row_base + c;
+    if (c + 4 <= n && (reinterpret_cast<uintptr_t>(p) & 15) == 0) {
+      *reinterpret_cast<f32x4*>(p) = v;
+    } else {
+#pragma unroll
+      for (int i = 0; i < 4; ++i)
+        if (c + i < n) p[i] = v[i];
+    }
+  }
+}
+
+// D[16][16] += A[16][128] B[128][16] with block scales.  Lane l: row (A) or
+// column (B) l % 16; with g = l / 16, fp4 registers 0-3 hold k = 32 g .. + 31,
+// fp8 registers 0-3 k = 16 g .. + 15 and registers 4-7 k = 64 + 16 g .. + 15;
+// the scale (low byte) is that of k block g.  D: row 4 (l / 16) + i, column
+// l % 16.
+template <int AF, int BF>
+__device__ __forceinline__ f32x4 mx_mfma16(const i32x8& a, const i32x8& b, const f32x4& c, uint32_t sa,
+                                           uint32_t sb) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+      a, b, c, AF == kMxFp8 ? 0 : 4, BF == kMxFp8 ? 0 : 4, 0, (int)sa, 0, (int)sb);
+}
+
 // D[32][32] += A[32][64] B[64][32] with block scales.  AF: format of A; B is
 // fp4.  Lane l: row (A) or column (B) l % 32.  With g = l / 32:
 //   fp4: registers 0-3 hold k = 32 g .. 32 g + 31, low nibble first;

@@ -104,13 +104,20 @@ __global__ __launch_bounds__(256) void mx_linear_kernel(MxProblem P) {
 
 }  // namespace
 
-int64_t mx_linear_blocks(const MxProblem& p) {
+// Products with few rows a weight: at most one tile of 16, or on average.
+static bool skinny(const MxProblem& p) {
+  return p.m <= 16 || (p.offsets && p.m <= 16 * (int64_t)p.experts);
+}
+
+int64_t mx_linear_blocks(int x_fmt, const MxProblem& p) {
+  if (skinny(p)) return mx_skinny_blocks(x_fmt, p);
   const int64_t tiles_m = (p.m + 63) / 64 + (p.offsets ? p.experts + 1 : 0);
   return tiles_m * ((p.n + 63) / 64);
 }
 
 hipError_t launch_mx_linear(int x_fmt, const MxProblem& p, hipStream_t stream) {
-  const dim3 grid((uint32_t)mx_linear_blocks(p));
+  if (skinny(p)) return launch_mx_skinny(x_fmt, p, stream);
+  const dim3 grid((uint32_t)mx_linear_blocks(x_fmt, p));
   if (p.offsets) {
     if (x_fmt == kMxFp8)
       mx_linear_kernel<kMxFp8, true><<<grid, dim3(256), 0, stream>>>(p);
