@@ -450,6 +450,8 @@ w4_status w4_gemv_batched(int32_t codec, int32_t m, int32_t y_dtype,
  */
 typedef enum { W4_MXFP4 = 0, W4_MXFP8 = 1 } w4_mx_format;
 
+/* Largest n of a product: keeps every per-block byte offset within 32 bits. */
+#define W4_MAX_MX_N 4194304
 /* Largest number of experts of a grouped product. */
 #define W4_MX_MAX_EXPERTS 4096
 
@@ -514,8 +516,13 @@ w4_status w4_mx_rmsnorm(int32_t format, int64_t rows, int64_t k, const void* x,
  * make their row's (column's) results NaN.
  * w, w_scales, x, x_scales 16-byte aligned.
  * Errors: W4_EINVAL (bad format, negative size, null pointer), W4_ESHAPE
- * (k % 32 != 0, k above W4_MAX_MATMUL_K, m above 2^31 - 1, too many tiles),
- * W4_EALIGN, W4_EUNSUPPORTED (y_dtype).
+ * (k % 32 != 0, k above W4_MAX_MATMUL_K, n above W4_MAX_MX_N, m above
+ * 2^31 - 1, too many tiles), W4_EALIGN, W4_EUNSUPPORTED (y_dtype), W4_EHIP.
+ * Workspace: with m > 16 and few output tiles the call may split k into S <= 8
+ * parts and enqueue a second kernel that adds their fp32 sums in order; those
+ * use S * m * n * 4 bytes that the library keeps per (device, stream) exactly
+ * as for w4_gemm (see there, also for capture into a graph).  With m <= 16 it
+ * uses none.
  */
 w4_status w4_mx_linear(int32_t x_format, int64_t n, int64_t k, const uint8_t* w,
                        const uint8_t* w_scales, const uint8_t* x, const uint8_t* x_scales,
@@ -536,7 +543,7 @@ w4_status w4_mx_linear(int32_t x_format, int64_t n, int64_t k, const uint8_t* w,
  * Accumulation, y_dtype, tolerance, alignment (offsets and row_index 4 bytes)
  * and errors as w4_mx_linear; also W4_ESHAPE for experts above
  * W4_MX_MAX_EXPERTS or tokens below rows without row_index.  experts == 0: y is
- * zeros.
+ * zeros.  No workspace.
  */
 w4_status w4_mx_grouped_linear(int32_t x_format, int32_t experts, int64_t n, int64_t k,
                                const uint8_t* w, const uint8_t* w_scales, int64_t tokens,

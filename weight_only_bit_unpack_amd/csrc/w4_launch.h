@@ -61,7 +61,7 @@ hipError_t launch_gemv_batched(int codec, const GemvProblem* probs_dev, int coun
 // user); its contents are undefined.  Growing allocates a new buffer and keeps
 // the old one (work already enqueued, or a graph captured earlier, may still
 // use it), so it never waits for the stream.
-enum { kWorkspaceGemm = 0, kWorkspaceGemv = 1 };
+enum { kWorkspaceGemm = 0, kWorkspaceGemv = 1, kWorkspaceMx = 2 };
 hipError_t stream_workspace(int user, hipStream_t stream, size_t bytes, char** out);
 
 // ws: a workspace of at least gemm_workspace_bytes(...) bytes, or nullptr for

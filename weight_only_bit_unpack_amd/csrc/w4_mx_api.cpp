@@ -39,7 +39,7 @@ w4_status check_array(int32_t format, int64_t rows, int64_t k) {
 
 w4_status check_product(int32_t x_format, int64_t n, int64_t k, int64_t m, int32_t y_dtype) {
   if (!valid_format(x_format) || n < 0 || k < 0 || m < 0) return W4_EINVAL;
-  if (k % 32 || k > W4_MAX_MATMUL_K || m > kMaxBlocks || n > kMaxBlocks) return W4_ESHAPE;
+  if (k % 32 || k > W4_MAX_MATMUL_K || n > W4_MAX_MX_N || m > kMaxBlocks) return W4_ESHAPE;
   if (y_dtype != W4_F32 && y_dtype != W4_BF16) return W4_EUNSUPPORTED;
   return W4_OK;
 }

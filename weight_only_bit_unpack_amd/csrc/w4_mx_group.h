@@ -26,38 +26,66 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v, F&& op) {
   return v;
 }
 
-// Tile t (the same in every lane) when each expert's rows, and at last the rows
-// of no expert, are cut into tiles of ROWS.  Every lane of the wave calls it.
-// 64 experts at a time, one a lane: the ends as a running maximum within
-// [0, rows], so that no offsets lead out of the buffers, then the tiles' sums.
-// A tile starts at row lo; the last tile of an expert may hold fewer rows.
+// The tiles when each expert's rows, and at last the rows of no expert, are cut
+// into tiles of ROWS.  A tile starts at row lo; the last one of an expert may
+// hold fewer rows.  The ends are read as a running maximum within [0, rows], so
+// that no offsets lead out of the buffers.  Every lane of the wave calls these.
 template <int ROWS>
-__device__ __forceinline__ GroupTile find_group_tile(const int32_t* offsets, int32_t experts,
-                                                     int32_t rows, uint32_t t) {
-  const int lane = threadIdx.x & 63;
-  uint32_t before = 0, at = 0;  // tiles and rows of the experts seen
-  for (int32_t c = 0; c <= experts; c += 64) {
+struct GroupScan {
+  const int32_t* offsets;
+  int32_t experts, rows;
+
+  // 64 experts from c on, one a lane: before, at -- tiles and rows of the
+  // experts before c.  lo, end: the expert's rows; upto: tiles up to and with it.
+  __device__ __forceinline__ void chunk(int32_t c, uint32_t before, uint32_t at, uint32_t& lo, uint32_t& end,
+                                        uint32_t& upto) const {
+    const int lane = threadIdx.x & 63;
     const int32_t e = c + lane;
     int32_t o = rows;
     if (e < experts) o = offsets[e + 1];
     o = o < 0 ? 0 : o > rows ? rows : o;
-    uint32_t end = (uint32_t)o > at ? (uint32_t)o : at;
+    end = (uint32_t)o > at ? (uint32_t)o : at;
     end = wave_scan(end, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
-    uint32_t lo = (uint32_t)__shfl_up((int)end, 1);
+    lo = (uint32_t)__shfl_up((int)end, 1);
     if (lane == 0) lo = at;
-    const uint32_t tiles = (end - lo + ROWS - 1) / ROWS;
-    const uint32_t upto = before + wave_scan(tiles, [](uint32_t a, uint32_t b) { return a + b; });
-    const uint64_t hit = __ballot(t < upto);
-    if (hit) {
-      const int f = __builtin_ctzll(hit);
-      const uint32_t first = (uint32_t)__builtin_amdgcn_readlane((int)(upto - tiles), f);
-      const int32_t l = __builtin_amdgcn_readlane((int)lo, f);
-      return GroupTile{c + f, l + (int32_t)(t - first) * ROWS, __builtin_amdgcn_readlane((int)end, f)};
-    }
-    before = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
-    at = (uint32_t)__builtin_amdgcn_readlane((int)end, 63);
+    upto = before + wave_scan((end - lo + ROWS - 1) / ROWS, [](uint32_t a, uint32_t b) { return a + b; });
   }
-  return GroupTile{-1, 0, 0};
-}
+
+  // tile t, the same in every lane
+  __device__ __forceinline__ GroupTile find(uint32_t t) const {
+    uint32_t before = 0, at = 0;
+    GroupTile g{-1, 0, 0};
+    for (int32_t c = 0; c <= experts; c += 64) {
+      uint32_t lo, end, upto;
+      chunk(c, before, at, lo, end, upto);
+      const uint64_t hit = __ballot(t < upto);
+      if (hit) {
+        const int f = __builtin_ctzll(hit);
+        const uint32_t first =
+            (uint32_t)__builtin_amdgcn_readlane((int)(upto - (end - lo + ROWS - 1) / ROWS), f);
+        g = GroupTile{c + f, __builtin_amdgcn_readlane((int)lo, f) + (int32_t)(t - first) * ROWS,
+                      __builtin_amdgcn_readlane((int)end, f)};
+        break;
+      }
+      before = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
+      at = (uint32_t)__builtin_amdgcn_readlane((int)end, 63);
+    }
+    // (the same in every lane: the addresses made from it stay scalar)
+    return GroupTile{__builtin_amdgcn_readfirstlane(g.e), __builtin_amdgcn_readfirstlane(g.lo),
+                     __builtin_amdgcn_readfirstlane(g.hi)};
+  }
+
+  // the number of tiles
+  __device__ __forceinline__ uint32_t count() const {
+    uint32_t before = 0, at = 0;
+    for (int32_t c = 0; c <= experts; c += 64) {
+      uint32_t lo, end, upto;
+      chunk(c, before, at, lo, end, upto);
+      before = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
+      at = (uint32_t)__builtin_amdgcn_readlane((int)end, 63);
+    }
+    return (uint32_t)__builtin_amdgcn_readfirstlane((int)before);
+  }
+};
 
 }  // namespace w4

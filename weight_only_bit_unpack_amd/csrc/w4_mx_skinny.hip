@@ -75,7 +75,7 @@ __global__ __launch_bounds__(KS * WN * 64) void mx_skinny_kernel(MxProblem P, ui
   const uint32_t nt = blockIdx.x % tiles_n;
   GroupTile T{0, 0, (int32_t)P.m};
   if constexpr (GROUPED) {
-    T = find_group_tile<kRows>(P.offsets, P.experts, (int32_t)P.m, blockIdx.x / tiles_n);
+    T = GroupScan<kRows>{P.offsets, P.experts, (int32_t)P.m}.find(blockIdx.x / tiles_n);
     if (T.e < 0) return;
   }
   const bool none = GROUPED && T.e == P.experts;  // rows of no expert
@@ -149,13 +149,13 @@ __global__ __launch_bounds__(KS * WN * 64) void mx_skinny_kernel(MxProblem P, ui
 #pragma unroll
       for (int j = 0; j < R; ++j) {
 #pragma unroll
-        for (int u = 0; u < 2; ++u) lw[j * 128 + (8 * u + lr) * 8 + (lc ^ lr)] = t.w[j][u];
+        for (int u = 0; u < 2; ++u) lw[j * 128 + (8 * u + lr) * 8 + (lc ^ ((4 * u + (lr >> 1)) & 7))] = t.w[j][u];
         t.ws[j].put(lws + j * 128, lane);
       }
 #pragma unroll
       for (int i = 0; i < XI; ++i) {
         const int row = 64 / XU * i + lane / XU;
-        lx[row * XU + ((lane ^ row) & (XU - 1))] = t.x[i];
+        lx[row * XU + ((lane ^ (XU == 16 ? row : row >> 1)) & (XU - 1))] = t.x[i];
       }
       t.xs.put(lxs, lane);
       wave_lds_sync();
@@ -167,13 +167,13 @@ __global__ __launch_bounds__(KS * WN * 64) void mx_skinny_kernel(MxProblem P, ui
           x0 = lx[xr * 16 + ((8 * u + g) ^ xr)];
           x1 = lx[xr * 16 + ((8 * u + 4 + g) ^ xr)];
         } else {
-          x0 = x1 = lx[xr * 8 + ((4 * u + g) ^ (xr & 7))];
+          x0 = x1 = lx[xr * 8 + ((4 * u + g) ^ (xr >> 1))];
         }
         const i32x8 b = mx_operand<AF>(x0, x1);
         const uint32_t sb = lxs[xr * 8 + 4 * u + g];
 #pragma unroll
         for (int j = 0; j < R; ++j) {
-          const u32x4 a = lw[j * 128 + r * 8 + ((4 * u + g) ^ (r & 7))];
+          const u32x4 a = lw[j * 128 + r * 8 + ((4 * u + g) ^ (r >> 1))];
           const uint32_t sa = lws[j * 128 + r * 8 + 4 * u + g];
           acc[j] = mx_mfma16<kMxFp4, AF>(mx_operand<kMxFp4>(a, a), b, acc[j], sa, sb);
         }
