@@ -23,7 +23,6 @@ W4_F32, W4_BF16, W4_F16 = 0, 1, 2
 GROUP = {W4_DYADIC: 64, W4_LUT16: 64, W4_SIGNMAG8: 32, W4_LUT16S: 64, W4_DYADIC5: 64,
          W4_LUT16S_PERM: 64, W4_LUT16S_IL: 64}
 W4_MXFP4, W4_MXFP8 = 0, 1  # MX formats (w4_mx_format)
-MX_BLOCK = 32  # values of an MX block
 IL_RECORD = 144  # bytes of one W4_LUT16S_IL record (256 weights)
 
 if not os.path.exists(LIB_PATH):
@@ -31,6 +30,7 @@ if not os.path.exists(LIB_PATH):
         f"{LIB_PATH} is missing: build it with `python weight_only_bit_unpack_amd/build.py`")
 
 _lib = ctypes.CDLL(LIB_PATH)
+from . import _w4mx  # noqa: E402  (links libw4.so; built with it)
 _P, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 
 
@@ -381,75 +381,32 @@ def w4_gemv_batched_plan(problems, codec=W4_DYADIC, y_dtype=torch.float32):
 
 
 # ------------------------------------------------------------------ MX (microscaled) operators
+# Checks, output tensors and the calls themselves are in _w4mx (C++,
+# csrc/w4_mx_binding.cpp): in Python they cost more than a small call's kernel.
 _MX_DTYPE = {torch.float32: W4_F32, torch.bfloat16: W4_BF16, torch.float16: W4_F16}
-_U8 = (torch.uint8,)
 
 
-def _mx_width(fmt, k):
-    """Bytes of k elements in a row."""
-    if fmt == W4_MXFP4:
-        return k // 2
-    if fmt == W4_MXFP8:
-        return k
-    raise ValueError(f"unknown MX format {fmt}")
+_w4mx.set_stream_query(
+    _raw_stream or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
 
 
-def _mx_k(fmt, q):
-    """k of an MX tensor from its elements' shape."""
-    return 2 * q.shape[-1] if fmt == W4_MXFP4 else q.shape[-1]
-
-
-def _mx_array(x, name, dev=None):
-    """rows, k and the dtype code of a dense [rows, k] input."""
-    _need(x, name, tuple(_MX_DTYPE), None, dev)
-    if x.dim() != 2:
-        raise ValueError(f"{name} must be [rows, k]")
-    rows, k = x.shape
-    if k % MX_BLOCK:
-        raise ValueError(f"{name} has rows of {k} values, expected a multiple of {MX_BLOCK}")
-    return rows, k, _MX_DTYPE[x.dtype]
-
-
-def _mx_out(q, scales, fmt, rows, k, like, dev):
-    """The elements and scales an MX output goes to, allocated where None."""
-    if q is None:
-        q = torch.empty((rows, _mx_width(fmt, k)), dtype=torch.uint8, device=like.device)
-    else:
-        _need(q, "q", _U8, (rows, _mx_width(fmt, k)), dev)
-    if scales is None:
-        scales = torch.empty((rows, k // MX_BLOCK), dtype=torch.uint8, device=like.device)
-    else:
-        _need(scales, "scales", _U8, (rows, k // MX_BLOCK), dev)
-    return q, scales
+def _mx_result(r):
+    """What _w4mx returned: the outputs, or the status of a refused call."""
+    if r.__class__ is int:
+        raise W4Error(r)
+    return r
 
 
 def w4_mx_quantize(x, fmt=W4_MXFP4, *, q=None, scales=None, stream=None):
     """Quantize x [rows, k] (fp32, bf16 or fp16; k a multiple of 32) to the MX
     form ``fmt`` (W4_MXFP4 or W4_MXFP8).  Returns (elements uint8 [rows, k/2]
     or [rows, k], scales uint8 [rows, k/32])."""
-    _need(x, "x", tuple(_MX_DTYPE))
-    dev = x.get_device()
-    rows, k, dt = _mx_array(x, "x", dev)
-    q, scales = _mx_out(q, scales, fmt, rows, k, x, dev)
-    _check(_lib.w4_mx_quantize(fmt, rows, k, x.data_ptr(), dt, q.data_ptr(), scales.data_ptr(),
-                               _stream(stream, dev)))
-    return q, scales
+    return _mx_result(_w4mx.quantize(x, fmt, q, scales, stream))
 
 
 def w4_mx_dequant(q, scales, fmt=W4_MXFP4, *, out=None, out_dtype=torch.bfloat16, stream=None):
     """The values of an MX tensor, bf16 or fp32 [rows, k]."""
-    _need(q, "q", _U8)
-    dev = q.get_device()
-    if q.dim() != 2:
-        raise ValueError("q must be [rows, k/2] or [rows, k]")
-    rows, k = q.shape[0], _mx_k(fmt, q)
-    _need(scales, "scales", _U8, (rows, k // MX_BLOCK), dev)
-    if out is None:
-        out = torch.empty((rows, k), dtype=out_dtype, device=q.device)
-    _need(out, "out", (torch.bfloat16, torch.float32), (rows, k), dev)
-    _check(_lib.w4_mx_dequant(fmt, rows, k, q.data_ptr(), scales.data_ptr(), out.data_ptr(),
-                              _MX_DTYPE[out.dtype], _stream(stream, dev)))
-    return out
+    return _mx_result(_w4mx.dequant(q, scales, fmt, out, _MX_DTYPE.get(out_dtype, -1), stream))
 
 
 def w4_mx_rmsnorm(x, gamma, eps=1e-6, fmt=W4_MXFP8, *, residual=None, residual_out=None, y=None,
@@ -461,65 +418,13 @@ def w4_mx_rmsnorm(x, gamma, eps=1e-6, fmt=W4_MXFP8, *, residual=None, residual_o
     like x) the norm itself is written there too, for what reads it
     unquantized; fmt=None writes only that and returns (None, None,
     residual_out)."""
-    _need(x, "x", tuple(_MX_DTYPE))
-    dev = x.get_device()
-    rows, k, dt = _mx_array(x, "x", dev)
-    like = (x.dtype,)
-    _need(gamma, "gamma", like, (k,), dev)
-    if residual is not None:
-        _need(residual, "residual", like, (rows, k), dev)
-        if residual_out is None:
-            residual_out = torch.empty_like(x)
-        else:
-            _need(residual_out, "residual_out", like, (rows, k), dev)
-    elif residual_out is not None:
-        raise ValueError("residual_out without a residual")
-    if y is not None:
-        _need(y, "y", like, (rows, k), dev)
-    if fmt is None:
-        if y is None:
-            raise ValueError("y is required without an MX format")
-        if q is not None or scales is not None:
-            raise ValueError("q or scales without an MX format")
-    else:
-        q, scales = _mx_out(q, scales, fmt, rows, k, x, dev)
-    _check(_lib.w4_mx_rmsnorm(W4_MXFP8 if fmt is None else fmt, rows, k, x.data_ptr(),
-                              _ptr(residual), gamma.data_ptr(), dt, eps, _ptr(residual_out),
-                              _ptr(y), _ptr(q), _ptr(scales), _stream(stream, dev)))
-    return q, scales, residual_out
-
-
-def _mx_y(y, y_dtype, m, n, like, dev):
-    if y is None:
-        if y_dtype not in (torch.float32, torch.bfloat16):
-            raise ValueError(f"y_dtype {y_dtype}, expected float32 or bfloat16")
-        return torch.empty((m, n), dtype=y_dtype, device=like.device)
-    return _need(y, "y", (torch.float32, torch.bfloat16), (m, n), dev)
-
-
-def _mx_x(xq, xs, fmt, k, dev):
-    """Checks the activations of a product against the weight's k; their rows."""
-    _need(xq, "xq", _U8, None, dev)
-    if xq.dim() != 2 or xq.shape[1] != _mx_width(fmt, k):
-        raise ValueError(f"xq has shape {tuple(xq.shape)}, expected [m, {_mx_width(fmt, k)}]")
-    _need(xs, "xs", _U8, (xq.shape[0], k // MX_BLOCK), dev)
-    return xq.shape[0]
+    return _mx_result(_w4mx.rmsnorm(x, gamma, eps, fmt, residual, residual_out, y, q, scales, stream))
 
 
 def w4_mx_linear(xq, xs, wq, ws, fmt=W4_MXFP8, *, y=None, y_dtype=torch.float32, stream=None):
     """y[m, n] = X[m, k] @ W[n, k]^T with X (xq, xs) in the MX form ``fmt`` and
     W (wq, ws) in W4_MXFP4; fp32 or bf16 y, any m."""
-    _need(wq, "wq", _U8)
-    dev = wq.get_device()
-    if wq.dim() != 2:
-        raise ValueError("wq must be [n, k/2]")
-    n, k = wq.shape[0], 2 * wq.shape[1]
-    _need(ws, "ws", _U8, (n, k // MX_BLOCK), dev)
-    m = _mx_x(xq, xs, fmt, k, dev)
-    y = _mx_y(y, y_dtype, m, n, wq, dev)
-    _check(_lib.w4_mx_linear(fmt, n, k, wq.data_ptr(), ws.data_ptr(), xq.data_ptr(), xs.data_ptr(),
-                             m, y.data_ptr(), _MX_DTYPE[y.dtype], _stream(stream, dev)))
-    return y
+    return _mx_result(_w4mx.linear(xq, xs, wq, ws, fmt, y, _MX_DTYPE.get(y_dtype, -1), stream))
 
 
 def w4_mx_grouped_linear(xq, xs, wq, ws, offsets, fmt=W4_MXFP8, *, rows=None, y=None,
@@ -530,23 +435,5 @@ def w4_mx_grouped_linear(xq, xs, wq, ws, offsets, fmt=W4_MXFP8, *, rows=None, y=
     offsets int32 [experts + 1] and rows int32 [number of rows of y] stay on the
     device.  Rows past the last offset, and rows whose index is outside X, are
     zeros."""
-    _need(wq, "wq", _U8)
-    dev = wq.get_device()
-    if wq.dim() != 3:
-        raise ValueError("wq must be [experts, n, k/2]")
-    experts, n, k = wq.shape[0], wq.shape[1], 2 * wq.shape[2]
-    _need(ws, "ws", _U8, (experts, n, k // MX_BLOCK), dev)
-    _need(offsets, "offsets", (torch.int32,), (experts + 1,), dev)
-    tokens = _mx_x(xq, xs, fmt, k, dev)
-    m = tokens
-    if rows is not None:
-        _need(rows, "rows", (torch.int32,), None, dev)
-        if rows.dim() != 1:
-            raise ValueError("rows must be [number of rows of y]")
-        m = rows.shape[0]
-    y = _mx_y(y, y_dtype, m, n, wq, dev)
-    _check(_lib.w4_mx_grouped_linear(fmt, experts, n, k, wq.data_ptr(), ws.data_ptr(), tokens,
-                                     xq.data_ptr(), xs.data_ptr(), m, offsets.data_ptr(),
-                                     _ptr(rows), y.data_ptr(), _MX_DTYPE[y.dtype],
-                                     _stream(stream, dev)))
-    return y
+    return _mx_result(_w4mx.grouped_linear(xq, xs, wq, ws, offsets, fmt, rows, y,
+                                           _MX_DTYPE.get(y_dtype, -1), stream))

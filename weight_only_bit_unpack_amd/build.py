@@ -2,9 +2,10 @@
 
     python weight_only_bit_unpack_amd/build.py
 
-Every source under csrc/ is compiled for gfx950 only; the objects go to
-csrc/_build/ and the shared library to this package directory, where the
-binding loads it from.
+Every source of the library under csrc/ is compiled for gfx950 only; the objects
+go to csrc/_build/ and the shared library to this package directory, where the
+binding loads it from.  The MX operators' part of the binding, _w4mx, is host
+code and is built beside it.
 """
 
 import os
@@ -57,9 +58,37 @@ CTX_SOURCES = ["ctx_read.hip"]
 CTX_LIB = os.path.join(PKG, "libw4ctx.so")
 
 
+# The MX operators' Python binding: host code against torch's C++ headers,
+# linked to libw4.so beside it.
+BINDING = "w4_mx_binding.cpp"
+BINDING_LIB = os.path.join(PKG, "_w4mx.so")
+CXX = os.environ.get("CXX", "g++")
+
+
+def _build_binding():
+    import sysconfig
+    import torch
+    base = os.path.dirname(torch.__file__)
+    inc = [sysconfig.get_paths()["include"], os.path.join(base, "include"),
+           os.path.join(base, "include", "torch", "csrc", "api", "include"),
+           os.path.join(ROOT, "include")]
+    lib = os.path.join(base, "lib")
+    tmp = BINDING_LIB + ".tmp"
+    cmd = [CXX, "-O2", "-std=c++17", "-shared", "-fPIC", "-fvisibility=hidden",
+           f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+           *[f"-isystem{i}" for i in inc], os.path.join(CSRC, BINDING), "-o", tmp,
+           LIB, f"-L{lib}", "-lc10", "-ltorch_cpu", "-ltorch", "-ltorch_python",
+           "-Wl,-rpath,$ORIGIN", f"-Wl,-rpath,{lib}"]
+    r = subprocess.run(cmd, capture_output=True, text=True)
+    if r.returncode != 0:
+        raise RuntimeError(f"{CXX} failed for {BINDING}:\n{r.stderr}")
+    os.replace(tmp, BINDING_LIB)
+
+
 def _link(objs, lib):
     tmp = lib + ".tmp"
-    cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp]
+    cmd = [HIPCC, f"--offload-arch={ARCH}", "-shared", "-fPIC", *objs, "-o", tmp,
+           f"-Wl,-soname,{os.path.basename(lib)}"]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         raise RuntimeError(f"link failed:\n{r.stderr}")
@@ -72,8 +101,9 @@ def build(verbose=False):
         objs = list(ex.map(_compile, SOURCES + CTX_SOURCES))
     _link(objs[:len(SOURCES)], LIB)
     _link(objs[len(SOURCES):], CTX_LIB)
+    _build_binding()
     if verbose:
-        print(f"built {LIB} and {CTX_LIB}")
+        print(f"built {LIB}, {CTX_LIB} and {BINDING_LIB}")
     return LIB
 
 
