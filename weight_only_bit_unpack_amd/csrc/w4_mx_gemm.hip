@@ -92,8 +92,11 @@ __global__ __launch_bounds__(T::THREADS) __attribute__((amdgpu_waves_per_eu(T::P
   // that they do make are dealt out.
   // (The grid is a multiple of 8.)
   uint32_t total = G.tiles_m * G.tiles_n * G.splits;
-  const GroupScan<T::BM> scan{P.offsets, P.experts, (int32_t)P.m};
-  if constexpr (GROUPED) total = scan.count() * G.tiles_n;
+  GroupScan<T::BM> scan(P.offsets, P.experts, (int32_t)P.m);
+  if constexpr (GROUPED) {
+    scan.read();
+    total = scan.count() * G.tiles_n;
+  }
   const uint32_t range = (total + 7) / 8, L = blockIdx.x % 8 * range + blockIdx.x / 8;
   if (blockIdx.x / 8 >= range || L >= total) return;
   uint32_t mt, nt, split = 0;

@@ -29,11 +29,16 @@ __device__ __forceinline__ uint32_t wave_scan(uint32_t v, F&& op) {
 // The tiles when each expert's rows, and at last the rows of no expert, are cut
 // into tiles of ROWS.  A tile starts at row lo; the last one of an expert may
 // hold fewer rows.  The ends are read as a running maximum within [0, rows], so
-// that no offsets lead out of the buffers.  Every lane of the wave calls these.
+// that no offsets lead out of the buffers.  Every lane of the wave calls these,
+// read() first.
 template <int ROWS>
 struct GroupScan {
   const int32_t* offsets;
   int32_t experts, rows;
+  uint32_t lo0 = 0, end0 = 0, upto0 = 0;  // the first 64 experts, once read
+
+  __device__ __forceinline__ GroupScan(const int32_t* o, int32_t e, int32_t r) : offsets(o), experts(e), rows(r) {}
+  __device__ __forceinline__ void read() { chunk(0, 0, 0, lo0, end0, upto0); }
 
   // 64 experts from c on, one a lane: before, at -- tiles and rows of the
   // experts before c.  lo, end: the expert's rows; upto: tiles up to and with it.
@@ -56,8 +61,8 @@ struct GroupScan {
     uint32_t before = 0, at = 0;
     GroupTile g{-1, 0, 0};
     for (int32_t c = 0; c <= experts; c += 64) {
-      uint32_t lo, end, upto;
-      chunk(c, before, at, lo, end, upto);
+      uint32_t lo = lo0, end = end0, upto = upto0;
+      if (c > 0) chunk(c, before, at, lo, end, upto);
       const uint64_t hit = __ballot(t < upto);
       if (hit) {
         const int f = __builtin_ctzll(hit);
@@ -79,8 +84,8 @@ struct GroupScan {
   __device__ __forceinline__ uint32_t count() const {
     uint32_t before = 0, at = 0;
     for (int32_t c = 0; c <= experts; c += 64) {
-      uint32_t lo, end, upto;
-      chunk(c, before, at, lo, end, upto);
+      uint32_t lo = lo0, end = end0, upto = upto0;
+      if (c > 0) chunk(c, before, at, lo, end, upto);
       before = (uint32_t)__builtin_amdgcn_readlane((int)upto, 63);
       at = (uint32_t)__builtin_amdgcn_readlane((int)end, 63);
     }

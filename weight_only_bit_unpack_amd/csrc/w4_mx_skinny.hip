@@ -75,7 +75,9 @@ __global__ __launch_bounds__(KS * WN * 64) void mx_skinny_kernel(MxProblem P, ui
   const uint32_t nt = blockIdx.x % tiles_n;
   GroupTile T{0, 0, (int32_t)P.m};
   if constexpr (GROUPED) {
-    T = GroupScan<kRows>{P.offsets, P.experts, (int32_t)P.m}.find(blockIdx.x / tiles_n);
+    GroupScan<kRows> scan(P.offsets, P.experts, (int32_t)P.m);
+    scan.read();
+    T = scan.find(blockIdx.x / tiles_n);
     if (T.e < 0) return;
   }
   const bool none = GROUPED && T.e == P.experts;  // rows of no expert
