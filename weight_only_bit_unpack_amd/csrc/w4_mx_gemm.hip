@@ -302,6 +302,20 @@ __global__ __launch_bounds__(T::THREADS) __attribute__((amdgpu_waves_per_eu(T::P
           asm volatile("" : "+v"(acc[i][j]));
         }
     };
+    // A quarter's products and the next one's reads by turns: the reads of eight
+    // waves issued together would fill the LDS queue, and the products would
+    // wait behind them.
+    auto interleave = [&]() {
+      constexpr int reads = T::NT + T::MT * (AF == kMxFp8 ? 2 : 1), products = T::MT * T::NT;
+#pragma unroll
+      for (int n = 0; n < products; ++n) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        if ((n + 1) * reads / products > n * reads / products)
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        if ((n + 1) * reads / products > n * reads / products + 1)
+          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      }
+    };
     using Q0 = std::integral_constant<int, 0>;
     using Q1 = std::integral_constant<int, 1>;
     using Q2 = std::integral_constant<int, 2>;
@@ -335,16 +349,16 @@ __global__ __launch_bounds__(T::THREADS) __attribute__((amdgpu_waves_per_eu(T::P
     shift_scales();
     for (uint32_t t = t0; t < t1; ++t) {
       read(o[1], t, Q1{});
-      __builtin_amdgcn_sched_barrier(0);
       multiply(o[0], Q0{});
+      interleave();
       __builtin_amdgcn_sched_barrier(0);
       read(o[0], t, Q2{});
-      __builtin_amdgcn_sched_barrier(0);
       multiply(o[1], Q1{});
+      interleave();
       __builtin_amdgcn_sched_barrier(0);
       read(o[1], t, Q3{});
-      __builtin_amdgcn_sched_barrier(0);
       multiply(o[0], Q2{});
+      interleave();
       __builtin_amdgcn_sched_barrier(0);
       if (t + 1 < t1) {
         // the next step's copies: all but those of the NS - 2 steps after it
