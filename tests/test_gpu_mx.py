@@ -280,7 +280,9 @@ LINEAR = [  # m, n, k
     (16, 31, 8192), (17, 64, 2080), (31, 129, 544), (32, 256, 2048), (33, 300, 96), (48, 128, 128),
     (64, 512, 4096), (65, 65, 1280), (100, 1000, 992), (127, 256, 5632), (128, 384, 224),
     (129, 127, 2048), (192, 130, 768), (256, 256, 1024), (257, 513, 2080), (300, 2048, 32), (511, 97, 4096),
-    (700, 700, 672), (1024, 512, 1024), (1030, 1100, 1120)]
+    (700, 700, 672), (1024, 512, 1024), (1030, 1100, 1120),
+    # rows of scales on whole dwords but no wider boundary
+    (40, 96, 384), (70, 300, 640), (200, 257, 1152), (600, 700, 2176)]
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
