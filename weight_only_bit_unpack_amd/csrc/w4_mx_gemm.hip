@@ -21,7 +21,7 @@ namespace {
 template <int AF, int BM_, int BN_, int WM_, int WN_, int NS_>
 struct Tile {
   static constexpr int NS = NS_;           // steps in LDS: one read, NS - 1 arriving
-  static constexpr int CS = NS / 2 + 1;    // scale slots
+  static constexpr int CS = NS == 4 ? 4 : 2;  // scale slots, at least NS / 2 + 1
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_;
   static constexpr int NW = WM * WN, THREADS = 64 * NW;
   static constexpr int MT = BM / WM / 32, NT = BN / WN / 32;
@@ -33,6 +33,9 @@ struct Tile {
   static constexpr int PER_CU = LDS * 16 <= 80 * 1024 ? 2 : 1;  // blocks of a CU
   static constexpr int IA = A / THREADS, IB = B / THREADS;     // copies of a wave per step
   static constexpr int IS = (S + THREADS - 1) / THREADS;       // scale rows of a thread
+  // quarters of a step whose operands are read ahead: two, where the registers
+  // hold them beside the accumulators
+  static constexpr int AHEAD = MT * NT < 8 ? 2 : 1;
   static_assert(IA * THREADS == A && IB * THREADS == B, "the waves share the copies");
 };
 
@@ -76,6 +79,8 @@ __device__ __forceinline__ void copy16(const uint8_t* base, uint32_t offset, uin
 
 // s_waitcnt for at most n vector memory operations in flight, the others free.
 constexpr int wait_vm(int n) { return (n & 15) | (n >> 4) << 14 | 0x0F70; }
+// s_waitcnt for every LDS operation, the others free.
+constexpr int kWaitLds = 0xC07F;
 
 template <int AF, typename T, bool GROUPED>
 __global__ __launch_bounds__(T::THREADS) __attribute__((amdgpu_waves_per_eu(T::PER_CU * T::NW / 4, T::PER_CU * T::NW / 4))) void mx_gemm_kernel(
@@ -146,9 +151,11 @@ __global__ __launch_bounds__(T::THREADS) __attribute__((amdgpu_waves_per_eu(T::P
     const uint32_t steps = (blocks + 7) / 8;
     const uint32_t t0 = (uint32_t)((uint64_t)split * steps / G.splits) & ~1u;
     const uint32_t t1 = split + 1 == G.splits ? steps : (uint32_t)((uint64_t)(split + 1) * steps / G.splits) & ~1u;
-    auto slot_a = [&](uint32_t t) { return lds + t % T::NS * T::A; };
-    auto slot_b = [&](uint32_t t) { return lds + T::NS * T::A + t % T::NS * T::B; };
-    auto slot_s = [&](uint32_t t) { return lds + T::NS * (T::A + T::B) + (t >> 1) % T::CS * T::S; };
+    // where a step's slots start, in units: ring of x and w by s = t % NS
+    auto slot_a = [](uint32_t s) { return s * T::A; };
+    auto slot_b = [](uint32_t s) { return T::NS * T::A + s * T::B; };
+    auto slot_s = [](uint32_t t) { return T::NS * (T::A + T::B) + (t >> 1) % T::CS * T::S; };
+    const uint32_t lds0 = lds_address(lds);
 
     // rows of the tile past the last one repeat it and are never stored
     auto row_of_x = [&](int i) {
@@ -167,33 +174,46 @@ __global__ __launch_bounds__(T::THREADS) __attribute__((amdgpu_waves_per_eu(T::P
     // Past the end of k a row's last unit is copied again: its scales are 0
     // there on both sides, and 2^-254 of anything finite adds nothing (a NaN
     // element is its row's already).
+    // 16-byte unit `lane` of a wave's copy i of x (w) in its row
+    auto unit_x = [&](int l, int i) {
+      const int u = (wave * T::IA + i) * 64 + l;
+      return 16u * swizzle<T::XU>(u / T::XU, u % T::XU);
+    };
+    auto unit_w = [&](int l, int i) {
+      const int u = (wave * T::IB + i) * 64 + l;
+      return 16u * swizzle<8>(u / 8, u % 8);
+    };
     const uint8_t* xp[T::IA];
-    uint32_t xo[T::IA];
 #pragma unroll
-    for (int i = 0; i < T::IA; ++i) {
-      const int u = (wave * T::IA + i) * 64 + lane, row = u / T::XU;
-      xp[i] = P.x + row_of_x(row) * x_bytes;
-      xo[i] = 16 * swizzle<T::XU>(row, u % T::XU);
-    }
-    uint32_t wp[T::IB], wo[T::IB];
+    for (int i = 0; i < T::IA; ++i)
+      xp[i] = P.x + row_of_x(((wave * T::IA + i) * 64 + lane) / T::XU) * x_bytes + unit_x(lane, i);
+    uint32_t wp[T::IB];  // (a block's rows: below 2^30 bytes)
 #pragma unroll
-    for (int i = 0; i < T::IB; ++i) {
-      const int u = (wave * T::IB + i) * 64 + lane, row = u / 8;
-      wp[i] = row_of_w(row) * half;  // (a block's rows: below 2^30 bytes)
-      wo[i] = 16 * swizzle<8>(row, u % 8);
-    }
-    // copy c of this wave's IA + IB of step t
+    for (int i = 0; i < T::IB; ++i)
+      wp[i] = row_of_w(((wave * T::IB + i) * 64 + lane) / 8) * half + unit_w(lane, i);
+    // this wave's copies of step t, to ring slot s; WHOLE: all of it lies before
+    // the end of k
     constexpr int C = T::IA + T::IB;
-    auto copy = [&](uint32_t t, int c) {
-      if (c < T::IA) {
-        const uint32_t o = xo[c < T::IA ? c : 0] + t * (16 * T::XU);
-        copy16(xp[c < T::IA ? c : 0] + (o < x_bytes ? o : x_bytes - 16),
-               lds_address(slot_a(t) + wave * T::IA * 64) + c * 1024);
-      } else {
-        const int i = c - T::IA;
-        const uint32_t o = wo[c < T::IA ? 0 : i] + t * 128;
-        copy16(wb, wp[c < T::IA ? 0 : i] + (o < half ? o : half - 16),
-               lds_address(slot_b(t) + wave * T::IB * 64) + i * 1024);
+    auto copy = [&](uint32_t t, uint32_t s, auto WHOLE) {
+      const uint32_t to_a = lds0 + 16 * (slot_a(s) + wave * T::IA * 64);
+      const uint32_t to_b = lds0 + 16 * (slot_b(s) + wave * T::IB * 64);
+      const uint32_t ox = t * (16 * T::XU), ow = t * 128;
+      int l = lane;
+      if (!decltype(WHOLE)::value) asm volatile("" : "+v"(l));  // (not worth registers from here on)
+#pragma unroll
+      for (int i = 0; i < T::IA; ++i) {
+        const uint32_t u = unit_x(l, i);
+        // (signed: a row can be shorter than the unit's offset)
+        const int32_t o = (int32_t)(decltype(WHOLE)::value || u + ox < x_bytes ? ox : x_bytes - 16 - u);
+        copy16(xp[i] + o, to_a + i * 1024);
+      }
+#pragma unroll
+      for (int i = 0; i < T::IB; ++i) {
+        const uint32_t u = unit_w(l, i);
+        if constexpr (decltype(WHOLE)::value)
+          copy16(uniform(wb + ow), wp[i], to_b + i * 1024);
+        else
+          copy16(wb, wp[i] + (u + ow < half ? ow : half - 16 - u), to_b + i * 1024);
       }
     };
     // Scales: 16 bytes (two steps) of a row at a time, a lane a row, copied like
@@ -212,7 +232,7 @@ __global__ __launch_bounds__(T::THREADS) __attribute__((amdgpu_waves_per_eu(T::P
 #pragma unroll
       for (int i = 0; i < T::IS; ++i)
         if (i * T::THREADS + wave * 64 < T::S)
-          copy16(sp[i] + 8 * t, lds_address(slot_s(t) + i * T::THREADS + wave * 64));
+          copy16(sp[i] + 8 * t, lds0 + 16 * (slot_s(t) + i * T::THREADS + wave * 64));
     };
     // (the last 16 bytes of a row, where fewer are left, and shifted when put)
     u32x4 sv[T::IS];
@@ -245,7 +265,7 @@ __global__ __launch_bounds__(T::THREADS) __attribute__((amdgpu_waves_per_eu(T::P
           v = (u32x4){__builtin_amdgcn_alignbyte(v.y, v.x, n), __builtin_amdgcn_alignbyte(v.z, v.y, n),
                       __builtin_amdgcn_alignbyte(v.w, v.z, n), __builtin_amdgcn_alignbyte(0u, v.w, n)};
         }
-        if (i * T::THREADS + wave * 64 < T::S) slot_s(t)[i * T::THREADS + tid] = v;
+        if (i * T::THREADS + wave * 64 < T::S) lds[slot_s(t) + i * T::THREADS + tid] = v;
       }
     };
 
@@ -253,12 +273,12 @@ __global__ __launch_bounds__(T::THREADS) __attribute__((amdgpu_waves_per_eu(T::P
     struct Operands {
       u32x4 a[T::MT][AF == kMxFp8 ? 2 : 1], b[T::NT];
     };
-    Operands o[2];
+    Operands o[2 * T::AHEAD];
     u32x2 sa[T::MT], sb[T::NT], na[T::MT], nb[T::NT];
-    auto read = [&](Operands& v, uint32_t t, auto Q) {
+    auto read = [&](Operands& v, uint32_t s, auto Q) {
       constexpr int q = decltype(Q)::value;
-      const u32x4* const a = slot_a(t);
-      const u32x4* const w = slot_b(t);
+      const u32x4* const a = lds + slot_a(s);
+      const u32x4* const w = lds + slot_b(s);
 #pragma unroll
       for (int j = 0; j < T::NT; ++j) {
         const int row = wn * (32 * T::NT) + 32 * j + r;
@@ -277,7 +297,7 @@ __global__ __launch_bounds__(T::THREADS) __attribute__((amdgpu_waves_per_eu(T::P
     };
     // the scale bytes of a row's eight blocks; lane half h needs blocks 2 q + h
     auto read_scales = [&](uint32_t t) {
-      const u32x2* const s = reinterpret_cast<const u32x2*>(slot_s(t)) + (t & 1);
+      const u32x2* const s = reinterpret_cast<const u32x2*>(lds + slot_s(t)) + (t & 1);
 #pragma unroll
       for (int i = 0; i < T::MT; ++i) na[i] = s[2 * (wm * (32 * T::MT) + 32 * i + r)];
 #pragma unroll
@@ -306,13 +326,12 @@ __global__ __launch_bounds__(T::THREADS) __attribute__((amdgpu_waves_per_eu(T::P
     // waves issued together would fill the LDS queue, and the products would
     // wait behind them.
     auto interleave = [&]() {
-      constexpr int reads = T::NT + T::MT * (AF == kMxFp8 ? 2 : 1), products = T::MT * T::NT;
+      constexpr int reads = T::AHEAD * (T::NT + T::MT * (AF == kMxFp8 ? 2 : 1)), products = T::AHEAD * T::MT * T::NT;
 #pragma unroll
       for (int n = 0; n < products; ++n) {
         __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-        if ((n + 1) * reads / products > n * reads / products)
-          __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-        if ((n + 1) * reads / products > n * reads / products + 1)
+#pragma unroll
+        for (int m = n * reads / products; m < (n + 1) * reads / products; ++m)
           __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
       }
     };
@@ -321,18 +340,72 @@ __global__ __launch_bounds__(T::THREADS) __attribute__((amdgpu_waves_per_eu(T::P
     using Q2 = std::integral_constant<int, 2>;
     using Q3 = std::integral_constant<int, 3>;
 
-    // Each quarter's operands are read while the quarter before is multiplied.
-    // The barrier of a step comes before its last quarter: by then every wave
-    // holds that quarter in registers, so the step's slot can take the copies
-    // of the step after next, and the next step's first quarter is read, while
-    // the last one is multiplied.
+    // A quarter's operands (AHEAD = 2: a half's) are read while the one before
+    // is multiplied.  The barrier of a step comes before its last quarter
+    // (half): by then every wave holds that in registers, so the step's slot can
+    // take the copies of step t + NS, and the next step's first operands are
+    // read, while it is multiplied.
+    // FAST: steps t + NS and t + 3 and their scales lie whole before the end of
+    // k, and all are copied: no conditions, and only x's addresses to add up.
+    uint32_t cur = t0 % T::NS;
+    auto step = [&](uint32_t t, auto FAST) {
+      constexpr bool fast = decltype(FAST)::value;
+      if constexpr (T::AHEAD == 2) {
+        read(o[2], cur, Q2{});
+        read(o[3], cur, Q3{});
+        multiply(o[0], Q0{});
+        multiply(o[1], Q1{});
+        interleave();
+      } else {
+        read(o[1], cur, Q1{});
+        multiply(o[0], Q0{});
+        interleave();
+        __builtin_amdgcn_sched_barrier(0);
+        read(o[0], cur, Q2{});
+        multiply(o[1], Q1{});
+        interleave();
+        __builtin_amdgcn_sched_barrier(0);
+        read(o[1], cur, Q3{});
+        multiply(o[0], Q2{});
+        interleave();
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      // the last operands (on every path here: after the branch the compiler's
+      // own wait would be for the next step's reads too)
+      __builtin_amdgcn_s_waitcnt(kWaitLds);
+      const uint32_t next = cur + 1 == T::NS ? 0 : cur + 1;
+      if (fast || t + 1 < t1) {
+        // the next step's copies: all but those of the NS - 2 steps after it
+        if (fast || t + T::NS <= t1)
+          __builtin_amdgcn_s_waitcnt(wait_vm((T::NS - 2) * C));
+        else
+          __builtin_amdgcn_s_waitcnt(wait_vm(0));
+        if (!fast && (t & 1) == 1 && !copied(t + 1)) put_scales(t + 1);
+        lds_barrier();
+        if (fast || t + T::NS < t1) {
+          if (((t + T::NS) & 1) == 0 && (fast || copied(t + T::NS))) copy_scales(t + T::NS);
+          copy(t + T::NS, cur, FAST);
+        }
+        if (!fast && (t & 1) == 1 && t + 3 < t1 && !copied(t + 3)) load_scales(t + 3);
+        read_scales(t + 1);
+        read(o[0], next, Q0{});
+        if constexpr (T::AHEAD == 2) read(o[1], next, Q1{});
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (T::AHEAD == 2) {
+        multiply(o[2], Q2{});
+        multiply(o[3], Q3{});
+      } else {
+        multiply(o[1], Q3{});
+      }
+      __builtin_amdgcn_sched_barrier(0);
+      shift_scales();
+      cur = next;
+    };
 #pragma unroll
     for (int i = 0; i < T::NS; ++i) {
       if (i % 2 == 0 && t0 + i < t1 && copied(t0 + i)) copy_scales(t0 + i);
-      if (t0 + i < t1) {
-#pragma unroll
-        for (int c = 0; c < C; ++c) copy(t0 + i, c);
-      }
+      if (t0 + i < t1) copy(t0 + i, (t0 + i) % T::NS, std::false_type{});
     }
     if (!copied(t0)) {
       load_scales(t0);
@@ -345,43 +418,17 @@ __global__ __launch_bounds__(T::THREADS) __attribute__((amdgpu_waves_per_eu(T::P
     lds_barrier();
     if (t0 + 2 < t1 && !copied(t0 + 2)) load_scales(t0 + 2);
     read_scales(t0);
-    read(o[0], t0, Q0{});
+    read(o[0], cur, Q0{});
+    if constexpr (T::AHEAD == 2) read(o[1], cur, Q1{});
     shift_scales();
-    for (uint32_t t = t0; t < t1; ++t) {
-      read(o[1], t, Q1{});
-      multiply(o[0], Q0{});
-      interleave();
-      __builtin_amdgcn_sched_barrier(0);
-      read(o[0], t, Q2{});
-      multiply(o[1], Q1{});
-      interleave();
-      __builtin_amdgcn_sched_barrier(0);
-      read(o[1], t, Q3{});
-      multiply(o[0], Q2{});
-      interleave();
-      __builtin_amdgcn_sched_barrier(0);
-      if (t + 1 < t1) {
-        // the next step's copies: all but those of the NS - 2 steps after it
-        if (t + T::NS <= t1)
-          __builtin_amdgcn_s_waitcnt(wait_vm((T::NS - 2) * C));
-        else
-          __builtin_amdgcn_s_waitcnt(wait_vm(0));
-        if ((t & 1) == 1 && !copied(t + 1)) put_scales(t + 1);
-        lds_barrier();
-        if (t + T::NS < t1) {
-          if (((t + T::NS) & 1) == 0 && copied(t + T::NS)) copy_scales(t + T::NS);
-#pragma unroll
-          for (int c = 0; c < C; ++c) copy(t + T::NS, c);
-        }
-        if ((t & 1) == 1 && t + 3 < t1 && !copied(t + 3)) load_scales(t + 3);
-        read_scales(t + 1);
-        read(o[0], t + 1, Q0{});
-      }
-      __builtin_amdgcn_sched_barrier(0);
-      multiply(o[1], Q3{});
-      __builtin_amdgcn_sched_barrier(0);
-      shift_scales();
-    }
+    // steps t with t + NS < t1 and 8 (t + max(NS, 3)) + 16 <= blocks
+    constexpr uint32_t reach = T::NS > 3 ? T::NS : 3;
+    const uint32_t inside = dwords && blocks >= 8 * reach + 16 ? (blocks - 16) / 8 - reach + 1 : 0;
+    const uint32_t tf = t1 < T::NS ? 0 : t1 - T::NS < inside ? t1 - T::NS : inside;
+    uint32_t t = t0;
+    if constexpr (T::AHEAD == 2)
+      for (; t < tf; ++t) step(t, std::true_type{});
+    for (; t < t1; ++t) step(t, std::false_type{});
   }
 
   if (GROUPED && (none || P.row_index)) {
@@ -511,7 +558,7 @@ struct Tiles<kMxFp8> {
   using T3 = Tile<kMxFp8, 64, 128, 2, 4, 4>;
   using T4 = Tile<kMxFp8, 64, 128, 2, 4, 2>;
   static constexpr Cost cost[5] = {
-      {5.4f, 1.67f, 0, 0}, {2.7f, 1.10f, 0, 0}, {3.3f, 1.08f, 0, 0}, {1.4f, 0.72f, 0, 0}, {0.9f, 0.75f, 2.3f, 1.12f}};
+      {5.6f, 1.58f, 0, 0}, {3.0f, 1.01f, 0, 0}, {2.2f, 1.06f, 0, 0}, {1.9f, 0.60f, 0, 0}, {1.2f, 0.69f, 4.0f, 1.05f}};
 };
 template <>
 struct Tiles<kMxFp4> {
@@ -521,7 +568,7 @@ struct Tiles<kMxFp4> {
   using T3 = Tile<kMxFp4, 64, 256, 1, 8, 3>;
   using T4 = Tile<kMxFp4, 64, 128, 2, 4, 3>;
   static constexpr Cost cost[5] = {
-      {7.0f, 2.05f, 0, 0}, {5.0f, 1.21f, 0, 0}, {2.1f, 0.80f, 0, 0}, {1.9f, 0.89f, 0, 0}, {0.8f, 0.59f, 2.5f, 0.91f}};
+      {6.7f, 2.04f, 0, 0}, {5.8f, 1.10f, 0, 0}, {3.0f, 0.70f, 0, 0}, {2.5f, 0.76f, 0, 0}, {1.0f, 0.46f, 3.3f, 0.80f}};
 };
 
 template <int AF, typename F>
@@ -545,10 +592,10 @@ struct Plan {
 
 // The tile and, for one weight, the parts of k that the costs above say take
 // the least time; the parts' sums cost a launch (3 us) and their bytes, written
-// and read, at 4 TB/s.  Examples (us, measured): 256 x 8192 x 8192, MXFP8, the
-// five tiles 53 / 35 / 36 / 27 / 27, the fourth is taken; 4096 x 11008 x 4096,
-// MXFP4, 128 / 158 / 187 / 210 / 196; 3001 rows over 7 experts of 2048 x 5632,
-// MXFP4, 47 / 38 / 49 / 53 / 51.
+// and read, at 4 TB/s.  Examples (us, measured, the five tiles, each
+// with its least parts): 256 x 8192 x 8192, MXFP8, 32 / 29 / 29 / 24 / 26, the
+// fourth is taken; 4096 x 11008 x 4096, MXFP4, 127 / 153 / 190 / 211 / 200; 3001
+// rows over 7 experts of 2048 x 5632, MXFP4, 45 / 33 / 41 / 42 / 42.
 template <int AF>
 Plan make_plan(const MxProblem& p) {
   const int64_t steps = (p.k + 255) / 256, cus = device_cus();
