@@ -303,6 +303,26 @@ def test_linear(w4, m, n, k, fmt, dtype):
     assert torch.equal(again, y)                    # the same bits every time
 
 
+# around the step counts at which a product's loop changes: 256 of k a step, 16
+# scales copied at a time, up to four steps in flight, and ends inside a step
+STEPS_K = [256 * s + d for s in (1, 2, 3, 4, 5, 6, 7, 9) for d in (-32, 0, 32, 128)]
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("m,n", [(40, 96), (150, 700), (600, 1100), (1100, 4200), (2300, 2900)])
+def test_linear_step_counts(w4, m, n, fmt):
+    g = torch.Generator("cuda").manual_seed(m + n)
+    for k in STEPS_K:
+        report("mx_linear_steps", m=m, n=n, k=k, fmt=fmt)
+        xq, xs = w4.w4_mx_quantize(torch.randn(m, k, generator=g, device="cuda"), code(w4, fmt))
+        wq, ws = w4.w4_mx_quantize(torch.randn(n, k, generator=g, device="cuda") * 0.02, w4.W4_MXFP4)
+        x = w4.w4_mx_dequant(xq, xs, code(w4, fmt), out_dtype=torch.float32).double()
+        w = w4.w4_mx_dequant(wq, ws, w4.W4_MXFP4, out_dtype=torch.float32).double()
+        y = w4.w4_mx_linear(xq, xs, wq, ws, code(w4, fmt))
+        wt = w.t().contiguous()
+        within(y, f64(x @ wt), f64(x.abs() @ wt.abs()), fmt, k)
+
+
 @pytest.mark.parametrize("fmt", FMTS)
 @pytest.mark.parametrize("m", [1, 4, 16, 40, 130, 300])
 def test_linear_every_element_in_its_place(w4, m, fmt):
