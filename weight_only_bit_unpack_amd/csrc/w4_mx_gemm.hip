@@ -365,8 +365,8 @@ __global__ __launch_bounds__(T::THREADS) __attribute__((amdgpu_waves_per_eu(T::P
     // (half): by then every wave holds that in registers, so the step's slot can
     // take the copies of step t + NS, and the next step's first operands are
     // read, while it is multiplied.
-    // FAST: steps t + NS and t + 3 and their scales lie whole before the end of
-    // k, and all are copied: no conditions, and only x's addresses to add up.
+    // FAST: step t + NS and the scales of steps t + NS and t + 3 lie whole before
+    // the end of k, or k is a multiple of 512, and so all are copied: no conditions, and only x's addresses to add up.
     uint32_t cur = t0 % T::NS;
     auto step = [&](uint32_t t, auto FAST) {
       constexpr bool fast = decltype(FAST)::value;
@@ -441,9 +441,11 @@ __global__ __launch_bounds__(T::THREADS) __attribute__((amdgpu_waves_per_eu(T::P
     read(o[0], cur, Q0{});
     if constexpr (T::AHEAD == 2) read(o[1], cur, Q1{});
     shift_scales();
-    // steps t with t + NS < t1 and 8 (t + max(NS, 3)) + 16 <= blocks
+    // steps t with t + NS < t1 and, unless every pair of steps is whole,
+    // 8 (t + max(NS, 3)) + 16 <= blocks
     constexpr uint32_t reach = T::NS > 3 ? T::NS : 3;
-    const uint32_t inside = dwords && blocks >= 8 * reach + 16 ? (blocks - 16) / 8 - reach + 1 : 0;
+    const uint32_t inside = blocks % 16 == 0 ? steps
+                            : dwords && blocks >= 8 * reach + 16 ? (blocks - 16) / 8 - reach + 1 : 0;
     const uint32_t tf = t1 < T::NS ? 0 : t1 - T::NS < inside ? t1 - T::NS : inside;
     uint32_t t = t0;
     if constexpr (T::AHEAD == 2)
