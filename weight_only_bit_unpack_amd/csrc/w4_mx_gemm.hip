@@ -404,7 +404,10 @@ __global__ __launch_bounds__(T::THREADS) __attribute__((amdgpu_waves_per_eu(T::P
         lds_barrier();
         if (fast || t + T::NS < t1) {
           if (((t + T::NS) & 1) == 0 && (fast || copied(t + T::NS))) copy_scales(t + T::NS);
-          copy(t + T::NS, cur, FAST);
+          if (fast || (T::AHEAD == 1 && 8 * (t + T::NS) + 8 <= blocks))
+            copy(t + T::NS, cur, std::true_type{});
+          else
+            copy(t + T::NS, cur, std::false_type{});
         }
         if (!fast && (t & 1) == 1 && t + 3 < t1 && !copied(t + 3)) load_scales(t + 3);
         read_scales(t + 1);
@@ -448,7 +451,7 @@ __global__ __launch_bounds__(T::THREADS) __attribute__((amdgpu_waves_per_eu(T::P
                             : dwords && blocks >= 8 * reach + 16 ? (blocks - 16) / 8 - reach + 1 : 0;
     const uint32_t tf = t1 < T::NS ? 0 : t1 - T::NS < inside ? t1 - T::NS : inside;
     uint32_t t = t0;
-    if constexpr (T::AHEAD == 2)
+    if constexpr (T::AHEAD == 2)  // (else a second loop's addresses would not fit the registers)
       for (; t < tf; ++t) step(t, std::true_type{});
     for (; t < t1; ++t) step(t, std::false_type{});
   }
