@@ -13,8 +13,9 @@
 // reaches 64 bytes a cycle and CU from L2, the steps need 20 to 30.
 //
 // Measured (HIP graph replays, operands larger than the L2): 4096 x 11008 x
-// 4096, MXFP4 to fp32, 127 us (2.9 PFLOP/s); 256 x 8192 x 8192, MXFP8 to bf16,
-// 23 us (1.5); 8192 rows over 32 experts of 4096 x 2048, MXFP8, 111 us (1.2);
+// 4096, MXFP4 to fp32, 125 us (3.0 PFLOP/s); 256 x 8192 x 8192, MXFP8 to bf16,
+// 23 us (1.5); 8192 rows over 32 experts of 4096 x 2048, MXFP8, 106 to 113 us by
+// machine (1.2 to 1.3);
 // 3001 rows over 7 experts of 2048 x 5632, MXFP4, 32 us (2.1).  Short k is held
 // by a tile's 4 to 8 us of start and end (the walk of the offsets, the first
 // copies, the stores, the next block's launch).
@@ -619,7 +620,7 @@ struct Plan {
 // the least time; the parts' sums cost a launch (3 us) and their bytes, written
 // and read, at 4 TB/s.  Examples (us, measured, the five tiles, each
 // with its least parts): 256 x 8192 x 8192, MXFP8, 32 / 29 / 29 / 24 / 26, the
-// fourth is taken; 4096 x 11008 x 4096, MXFP4, 127 / 153 / 190 / 211 / 200; 3001
+// fourth is taken; 4096 x 11008 x 4096, MXFP4, 125 / 153 / 190 / 211 / 200; 3001
 // rows over 7 experts of 2048 x 5632, MXFP4, 45 / 33 / 41 / 42 / 42.
 template <int AF>
 Plan make_plan(const MxProblem& p) {
