@@ -486,8 +486,9 @@ w4_status w4_mx_dequant(int32_t format, int64_t rows, int64_t k, const uint8_t* 
  * (W4_F32, W4_BF16, W4_F16) of x, residual, gamma, residual_out and y:
  *   h = x + residual in fp32, rounded to T (RNE) and written to residual_out
  *       (residual == NULL: h = x, residual_out is not used);
- *   v = h * gamma / sqrt(sum_c h^2 / k + eps) in fp32 (the row's factor is
- *       computed in fp64 from fp32 partial sums);
+ *   v = h * gamma / sqrt(sum_c h^2 / k + eps): the sum and the row's factor
+ *       in fp64, v within 4 * 2^-24 of it in fp32 for every finite h whose v
+ *       is a normal fp32 number;
  *   y = RNE_T(v) unless y is NULL; elements, scales = w4_mx_quantize(v) unless
  *       elements is NULL.  One of the two must be given.
  * The sums are the same bits for the same shape.  A NaN or an infinity in a row

@@ -1,0 +1,75 @@
+"""MX operators on the GPU at the ends of their ranges, against the fp64 oracle
+(oracle/mx.py).
+
+Tolerance of the norm, from the arithmetic: the squares add up in fp64 and the
+row's factor is a power of two, applied exactly, times a number that is rounded
+to fp32 once; a value then takes two fp32 roundings, the factor's product and
+gamma's.  So v = v_exact (1 + d), |d| <= tau = 4 * 2^-24, wherever v is a normal
+fp32 number, and codes are those of some number in [v (1 - tau), v (1 + tau)].
+"""
+
+import numpy as np
+import pytest
+import torch
+
+from oracle import mx
+from tests.gpu_util import report
+from tests.test_gpu_mx import DT, FMTS, check_codes, code, dev, f64, rounded
+
+pytestmark = pytest.mark.gpu
+
+TAU = 4 * 2.0 ** -24
+
+
+@pytest.fixture(scope="module")
+def w4():
+    import weight_only_bit_unpack_amd as m
+    return m
+
+
+# ------------------------------------------------------------------ RMS norm
+def norm_matches(w4, x, gamma, eps, fmt, dt, residual=None):
+    t, gm = dev(x, dt), dev(gamma, dt)
+    y = torch.full_like(t, float("nan"))
+    r = None if residual is None else dev(residual, dt)
+    q, s, _ = w4.w4_mx_rmsnorm(t, gm, eps, code(w4, fmt), residual=r, y=y)
+    h = f64(t) if r is None else rounded((f64(t) + f64(r)).astype(np.float32).astype(np.float64), dt)
+    v = mx.rmsnorm(h, f64(gm), eps)
+    check_codes(q.cpu().numpy(), s.cpu().numpy(), v, TAU, fmt)
+    a, b = rounded(v * (1 - TAU), dt), rounded(v * (1 + TAU), dt)
+    got = f64(y)
+    assert ((np.minimum(a, b) <= got) & (got <= np.maximum(a, b))).all()
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("fmt", FMTS)
+@pytest.mark.parametrize("size", [1e-40, 1e-25, 1e-19, 1e19, 1e25, 8e37])
+def test_rmsnorm_large_and_small_rows(w4, size, fmt, dt):
+    """Finite rows whose squares pass fp32's range on either side."""
+    report("mx_rmsnorm_range", size=size, fmt=fmt, dt=dt)
+    g = np.random.default_rng(3)
+    for rows, k in ((3, 32), (5, 512), (2, 4128)):
+        x = np.clip(g.standard_normal((rows, k)), -4, 4) * size
+        gamma = 1 + 0.2 * g.standard_normal(k)
+        norm_matches(w4, x, gamma, 0.0, fmt, dt)
+        norm_matches(w4, x, gamma, 0.0, fmt, dt, residual=np.zeros_like(x))
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_rmsnorm_one_large_value(w4, fmt):
+    """One value far above the others: theirs are small, not zero."""
+    report("mx_rmsnorm_one_large", fmt=fmt)
+    g = np.random.default_rng(4)
+    x = 1 + g.random((4, 512))
+    x[[0, 1, 2], [0, 300, 511]] = 3e38, -1e30, 1e20
+    norm_matches(w4, x, np.ones(512), 1e-6, fmt, "f32")
+
+
+@pytest.mark.parametrize("fmt", FMTS)
+def test_rmsnorm_gamma_and_row_of_opposite_size(w4, fmt):
+    """h * gamma passes fp32's range on either side, the norm does not."""
+    report("mx_rmsnorm_gamma_range", fmt=fmt)
+    g = np.random.default_rng(5)
+    x = g.standard_normal((3, 256))
+    for size, scale in ((1e30, 1e12), (1e-30, 1e-12)):
+        norm_matches(w4, x * size, scale * (1 + g.random(256)), 0.0, fmt, "f32")

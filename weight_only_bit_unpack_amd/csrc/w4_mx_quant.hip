@@ -70,10 +70,12 @@ __global__ __launch_bounds__(256) void mx_dequant_kernel(const uint8_t* __restri
 }
 
 // ---------------------------------------------------------------- RMS norm
-// One row per block.  The squares of a lane's values add up in fp32, the
-// lanes in fp64, so that the row's one factor 1 / sqrt(mean + eps) is right to
-// fp32's last place or so; each value then takes two roundings, (r * gamma) and
-// the product with the factor, before the element's own.  The second pass reads
+// One row per block.  The squares add up in fp64, which holds those of every
+// fp32 number without overflow or underflow, at no cost beside the row's
+// memory.  The row's factor 1 / sqrt(mean + eps), which can lie outside
+// fp32's range as well, is applied as a power of two, exactly, and a number in
+// [1/2, 1) rounded to fp32; gamma comes after it, when the row is of size one.
+// So a value takes two roundings more before the element's own.  The second pass reads
 // the row back through L2 (8 KB at k = 4096, just written or read by this block),
 // not from HBM: the kernel runs at the card's copy rate without holding the row
 // in registers, and k has no bound.
@@ -85,7 +87,7 @@ __global__ __launch_bounds__(256) void mx_rmsnorm_kernel(const void* x, const vo
   const int64_t C = k >> 3;  // groups of eight in a row
   const int64_t r0 = (int64_t)blockIdx.x * C;
   const int tid = threadIdx.x;
-  float ss = 0.f;
+  double t = 0.0;
   for (int64_t c = tid; c < C; c += 256) {
     float v[8];
     to_f32<DT>(load8<DT>(x, r0 + c), v);
@@ -99,23 +101,25 @@ __global__ __launch_bounds__(256) void mx_rmsnorm_kernel(const void* x, const vo
       to_f32<DT>(h, v);
     }
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss += v[i] * v[i];
+    for (int i = 0; i < 8; ++i) t = __builtin_fma((double)v[i], (double)v[i], t);
   }
-  double t = ss;
 #pragma unroll
   for (int o = 32; o; o >>= 1) t += __shfl_xor(t, o);
   __shared__ double part[4];
   if ((tid & 63) == 0) part[tid >> 6] = t;
   __syncthreads();
   t = (part[0] + part[1]) + (part[2] + part[3]);
-  const float f = (float)(1.0 / __builtin_sqrt(t / (double)k + (double)eps));
+  // (0, infinity and NaN have exponent 0 here and stay what they are)
+  const double factor = 1.0 / __builtin_sqrt(t / (double)k + (double)eps);
+  const int e = __builtin_amdgcn_frexp_exp(factor);
+  const float f = (float)__builtin_amdgcn_frexp_mant(factor);
   const void* h = residual ? residual_out : x;  // a thread reads back what it wrote itself
   for (int64_t c = tid; c < C; c += 256) {
     float v[8], w[8];
     to_f32<DT>(load8<DT>(h, r0 + c), v);
     to_f32<DT>(load8<DT>(gamma, c), w);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) v[i] = v[i] * w[i] * f;
+    for (int i = 0; i < 8; ++i) v[i] = __builtin_ldexpf(v[i], e) * f * w[i];
     if (y) store8<DT>(y, r0 + c, from_f32<DT>(v));
     if (q) {
       uint32_t b, e[2];
