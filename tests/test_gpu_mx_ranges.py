@@ -14,7 +14,7 @@ import torch
 
 from oracle import mx
 from tests.gpu_util import report
-from tests.test_gpu_mx import DT, FMTS, check_codes, code, dev, f64, rounded
+from tests.test_gpu_mx import FMTS, _chain, _chain_inputs, check_codes, code, dev, f64, rounded
 
 pytestmark = pytest.mark.gpu
 
@@ -73,3 +73,61 @@ def test_rmsnorm_gamma_and_row_of_opposite_size(w4, fmt):
     x = g.standard_normal((3, 256))
     for size, scale in ((1e30, 1e12), (1e-30, 1e-12)):
         norm_matches(w4, x * size, scale * (1 + g.random(256)), 0.0, fmt, "f32")
+
+
+# ------------------------------------------------------------------ streams
+def stream_calls(w4):
+    """Every operator with outputs of its own, and its inputs."""
+    g = torch.Generator("cuda").manual_seed(1)
+    x = torch.randn(64, 512, generator=g, device="cuda").bfloat16()
+    gm = torch.ones(512, device="cuda").bfloat16()
+    xq, xs = w4.w4_mx_quantize(x, w4.W4_MXFP8)
+    wq, ws = w4.w4_mx_quantize(torch.randn(256, 512, generator=g, device="cuda"))
+    off = torch.tensor([0, 30, 64], dtype=torch.int32, device="cuda")
+    wg, wgs = wq.view(2, 128, 256), ws.view(2, 128, 16)
+    return [
+        lambda **s: w4.w4_mx_quantize(x, w4.W4_MXFP8, **s),
+        lambda **s: (w4.w4_mx_dequant(xq, xs, w4.W4_MXFP8, **s),),
+        lambda **s: w4.w4_mx_rmsnorm(x, gm, residual=x, **s),
+        lambda **s: (w4.w4_mx_linear(xq, xs, wq, ws, **s),),
+        lambda **s: (w4.w4_mx_grouped_linear(xq, xs, wg, wgs, off, **s),)]
+
+
+@pytest.mark.parametrize("op", range(5))
+def test_stream_argument_allocates_on_that_stream(w4, op):
+    """With stream= the outputs that the call makes are that stream's: a block just
+    freed on the caller's stream, where queued work may still use it, is not taken."""
+    report("mx_stream_outputs", op=op)
+    call = stream_calls(w4)[op]
+    side = torch.cuda.Stream()
+    want = [t.clone() for t in call()]
+    torch.cuda.synchronize()
+    mine = call()
+    freed = {t.data_ptr() for t in mine}
+    del mine                                         # back to the caller's stream's pool
+    torch.cuda.synchronize()
+    got = call(stream=side)
+    assert not freed & {t.data_ptr() for t in got}
+    side.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert torch.cuda.current_stream() == torch.cuda.default_stream()
+
+
+@pytest.mark.parametrize("tokens", [1, 200])
+def test_stream_argument_runs_there(w4, tokens):
+    """The chain of calls given stream= equals the chain on the current stream, and
+    waits for that stream's own work only."""
+    report("mx_stream_argument", tokens=tokens)
+    a = _chain_inputs(np.random.default_rng(tokens), tokens)
+    _chain(w4, *a)
+    torch.cuda.synchronize()
+    want = [a[9].clone(), a[10].clone()]
+    x, side = a[0].clone(), torch.cuda.Stream()
+    for rep in range(3):
+        a[0].zero_(), a[9].fill_(float("nan")), a[10].fill_(float("nan"))
+        torch.cuda.synchronize()
+        with torch.cuda.stream(side):
+            a[0].copy_(x)                            # before the calls in the side stream's order
+        _chain(w4, *a, stream=side)
+        side.synchronize()
+        assert torch.equal(a[9], want[0]) and torch.equal(a[10], want[1]), rep

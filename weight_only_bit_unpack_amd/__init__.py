@@ -383,6 +383,9 @@ def w4_gemv_batched_plan(problems, codec=W4_DYADIC, y_dtype=torch.float32):
 # ------------------------------------------------------------------ MX (microscaled) operators
 # Checks, output tensors and the calls themselves are in _w4mx (C++,
 # csrc/w4_mx_binding.cpp): in Python they cost more than a small call's kernel.
+# ``stream`` works as ``with torch.cuda.stream(stream)`` around the call: outputs
+# are that stream's tensors, and inputs made on another one have to be ready and
+# kept (Tensor.record_stream) as for torch's own operators.
 _MX_DTYPE = {torch.float32: W4_F32, torch.bfloat16: W4_BF16, torch.float16: W4_F16}
 
 
@@ -390,9 +393,17 @@ _w4mx.set_stream_query(
     _raw_stream or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
 
 
-def _mx_result(r):
-    """What _w4mx returned: the outputs, or the status of a refused call."""
-    if r.__class__ is int:
+def _mx(stream, call, *args):
+    """The outputs of a call of _w4mx, or the error of a refused one.  It works
+    on the current stream, which ``stream`` is made for the call, so that outputs
+    come from that stream's part of the allocator: a block of the caller's
+    stream could still be in use by work queued there."""
+    if stream is None:
+        r = call(*args)
+    else:
+        with torch.cuda.stream(stream):
+            r = call(*args)
+    if r.__class__ is int:  # a status
         raise W4Error(r)
     return r
 
@@ -401,12 +412,12 @@ def w4_mx_quantize(x, fmt=W4_MXFP4, *, q=None, scales=None, stream=None):
     """Quantize x [rows, k] (fp32, bf16 or fp16; k a multiple of 32) to the MX
     form ``fmt`` (W4_MXFP4 or W4_MXFP8).  Returns (elements uint8 [rows, k/2]
     or [rows, k], scales uint8 [rows, k/32])."""
-    return _mx_result(_w4mx.quantize(x, fmt, q, scales, stream))
+    return _mx(stream, _w4mx.quantize, x, fmt, q, scales)
 
 
 def w4_mx_dequant(q, scales, fmt=W4_MXFP4, *, out=None, out_dtype=torch.bfloat16, stream=None):
     """The values of an MX tensor, bf16 or fp32 [rows, k]."""
-    return _mx_result(_w4mx.dequant(q, scales, fmt, out, _MX_DTYPE.get(out_dtype, -1), stream))
+    return _mx(stream, _w4mx.dequant, q, scales, fmt, out, _MX_DTYPE.get(out_dtype, -1))
 
 
 def w4_mx_rmsnorm(x, gamma, eps=1e-6, fmt=W4_MXFP8, *, residual=None, residual_out=None, y=None,
@@ -418,13 +429,13 @@ def w4_mx_rmsnorm(x, gamma, eps=1e-6, fmt=W4_MXFP8, *, residual=None, residual_o
     like x) the norm itself is written there too, for what reads it
     unquantized; fmt=None writes only that and returns (None, None,
     residual_out)."""
-    return _mx_result(_w4mx.rmsnorm(x, gamma, eps, fmt, residual, residual_out, y, q, scales, stream))
+    return _mx(stream, _w4mx.rmsnorm, x, gamma, eps, fmt, residual, residual_out, y, q, scales)
 
 
 def w4_mx_linear(xq, xs, wq, ws, fmt=W4_MXFP8, *, y=None, y_dtype=torch.float32, stream=None):
     """y[m, n] = X[m, k] @ W[n, k]^T with X (xq, xs) in the MX form ``fmt`` and
     W (wq, ws) in W4_MXFP4; fp32 or bf16 y, any m."""
-    return _mx_result(_w4mx.linear(xq, xs, wq, ws, fmt, y, _MX_DTYPE.get(y_dtype, -1), stream))
+    return _mx(stream, _w4mx.linear, xq, xs, wq, ws, fmt, y, _MX_DTYPE.get(y_dtype, -1))
 
 
 def w4_mx_grouped_linear(xq, xs, wq, ws, offsets, fmt=W4_MXFP8, *, rows=None, y=None,
@@ -435,5 +446,5 @@ def w4_mx_grouped_linear(xq, xs, wq, ws, offsets, fmt=W4_MXFP8, *, rows=None, y=
     offsets int32 [experts + 1] and rows int32 [number of rows of y] stay on the
     device.  Rows past the last offset, and rows whose index is outside X, are
     zeros."""
-    return _mx_result(_w4mx.grouped_linear(xq, xs, wq, ws, offsets, fmt, rows, y,
-                                           _MX_DTYPE.get(y_dtype, -1), stream))
+    return _mx(stream, _w4mx.grouped_linear, xq, xs, wq, ws, offsets, fmt, rows, y,
+               _MX_DTYPE.get(y_dtype, -1))

@@ -126,26 +126,20 @@ Tensor product_output(PyObject* o, long y_dtype, int64_t m, int64_t n, const Ten
 const uint8_t* u8(const Tensor& t) { return static_cast<const uint8_t*>(t.const_data_ptr()); }
 uint8_t* u8(Tensor& t) { return static_cast<uint8_t*>(t.data_ptr()); }
 
-// The HIP stream of a call: the given torch stream's, else the current one of
-// the device, which `query` (set by __init__.py) names.
+// The current HIP stream of the device, which `query` (set by __init__.py)
+// names.  The outputs' memory is this stream's too.
 PyObject* query = nullptr;
 
-struct Stream {
-  void* handle = nullptr;
-  Stream(PyObject* o, int dev) {
-    PyObject* v = nullptr;
-    if (o != Py_None) {
-      v = PyObject_GetAttrString(o, "cuda_stream");
-    } else if (query) {
-      PyObject* d = PyLong_FromLong(dev);
-      v = PyObject_CallFunctionObjArgs(query, d, nullptr);
-      Py_XDECREF(d);
-    }
-    if (v) handle = PyLong_AsVoidPtr(v);
-    Py_XDECREF(v);
-    if (!v || PyErr_Occurred()) throw PythonError();
-  }
-};
+void* stream(int dev) {
+  if (PyErr_Occurred()) throw PythonError();  // (from reading an argument)
+  PyObject* d = PyLong_FromLong(dev);
+  PyObject* v = query && d ? PyObject_CallFunctionObjArgs(query, d, nullptr) : nullptr;
+  Py_XDECREF(d);
+  void* handle = v ? PyLong_AsVoidPtr(v) : nullptr;
+  Py_XDECREF(v);
+  if (PyErr_Occurred()) throw PythonError();
+  return handle;
+}
 
 PyObject* pair(const Tensor& a, const Tensor& b) {
   PyObject* r = PyTuple_New(2);
@@ -180,9 +174,9 @@ PyObject* guarded(Py_ssize_t got, Py_ssize_t n, F&& f) {
   return nullptr;
 }
 
-// (x, fmt, q, scales, stream) -> (q, scales)
+// (x, fmt, q, scales) -> (q, scales)
 PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 5, [&]() -> PyObject* {
+  return guarded(n, 4, [&]() -> PyObject* {
     const int dev = current_device(a[0], "x");
     const Tensor& x = dense(a[0], "x", dev);
     const long fmt = PyLong_AsLong(a[1]);
@@ -190,14 +184,14 @@ PyObject* quantize(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Tensor q = byte_output(a[2], "q", {rows, width(fmt, k)}, x, dev);
     Tensor s = byte_output(a[3], "scales", {rows, k / 32}, x, dev);
     const w4_status st = w4_mx_quantize(fmt, rows, k, x.const_data_ptr(), dtype_code(x.scalar_type()), u8(q), u8(s),
-                                        Stream(a[4], dev).handle);
+                                        stream(dev));
     return st ? status(st) : pair(q, s);
   });
 }
 
-// (q, scales, fmt, out, out_dtype, stream) -> out
+// (q, scales, fmt, out, out_dtype) -> out
 PyObject* dequant(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 6, [&]() -> PyObject* {
+  return guarded(n, 5, [&]() -> PyObject* {
     const int dev = current_device(a[0], "q");
     const Tensor& q = bytes(a[0], "q", dev);
     const long fmt = PyLong_AsLong(a[2]), code = PyLong_AsLong(a[4]);
@@ -218,15 +212,15 @@ PyObject* dequant(PyObject*, PyObject* const* a, Py_ssize_t n) {
       need_shape(out, "out", {rows, k});
     }
     const w4_status st =
-        w4_mx_dequant(fmt, rows, k, u8(q), u8(s), out.data_ptr(), dtype_code(out.scalar_type()), Stream(a[5], dev).handle);
+        w4_mx_dequant(fmt, rows, k, u8(q), u8(s), out.data_ptr(), dtype_code(out.scalar_type()), stream(dev));
     return st ? status(st) : THPVariable_Wrap(out);
   });
 }
 
-// (x, gamma, eps, fmt or None, residual, residual_out, y, q, scales, stream)
+// (x, gamma, eps, fmt or None, residual, residual_out, y, q, scales)
 // -> (q, scales, residual_out)
 PyObject* rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 10, [&]() -> PyObject* {
+  return guarded(n, 9, [&]() -> PyObject* {
     const int dev = current_device(a[0], "x");
     const Tensor& x = dense(a[0], "x", dev);
     const int64_t rows = x.size(0), k = x.size(1);
@@ -261,7 +255,7 @@ PyObject* rmsnorm(PyObject*, PyObject* const* a, Py_ssize_t n) {
     }
     const w4_status st = w4_mx_rmsnorm(fmt, rows, k, x.const_data_ptr(), residual, gamma.const_data_ptr(),
                                        dtype_code(dt), (float)eps, residual ? ro.data_ptr() : nullptr, y,
-                                       mx ? u8(q) : nullptr, mx ? u8(s) : nullptr, Stream(a[9], dev).handle);
+                                       mx ? u8(q) : nullptr, mx ? u8(s) : nullptr, stream(dev));
     if (st) return status(st);
     PyObject* r = PyTuple_New(3);
     if (!r) return nullptr;
@@ -289,9 +283,9 @@ int64_t activations(const Tensor& xq, const Tensor& xs, long fmt, int64_t k) {
   return xq.size(0);
 }
 
-// (xq, xs, wq, ws, fmt, y, y_dtype, stream) -> y
+// (xq, xs, wq, ws, fmt, y, y_dtype) -> y
 PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 8, [&]() -> PyObject* {
+  return guarded(n, 7, [&]() -> PyObject* {
     const int dev = current_device(a[2], "wq");
     const Tensor& wq = bytes(a[2], "wq", dev);
     if (wq.dim() != 2) throw Refused("wq must be [n, k/2]");
@@ -304,14 +298,14 @@ PyObject* linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t m = activations(xq, xs, fmt, k);
     Tensor y = product_output(a[5], PyLong_AsLong(a[6]), m, rows, wq, dev);
     const w4_status st = w4_mx_linear(fmt, rows, k, u8(wq), u8(ws), u8(xq), u8(xs), m, y.data_ptr(),
-                                      dtype_code(y.scalar_type()), Stream(a[7], dev).handle);
+                                      dtype_code(y.scalar_type()), stream(dev));
     return st ? status(st) : THPVariable_Wrap(y);
   });
 }
 
-// (xq, xs, wq, ws, offsets, fmt, rows or None, y, y_dtype, stream) -> y
+// (xq, xs, wq, ws, offsets, fmt, rows or None, y, y_dtype) -> y
 PyObject* grouped_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
-  return guarded(n, 10, [&]() -> PyObject* {
+  return guarded(n, 9, [&]() -> PyObject* {
     const int dev = current_device(a[2], "wq");
     const Tensor& wq = bytes(a[2], "wq", dev);
     if (wq.dim() != 3) throw Refused("wq must be [experts, n, k/2]");
@@ -338,7 +332,7 @@ PyObject* grouped_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     Tensor y = product_output(a[7], PyLong_AsLong(a[8]), m, cols, wq, dev);
     const w4_status st = w4_mx_grouped_linear(fmt, (int32_t)experts, cols, k, u8(wq), u8(ws), tokens, u8(xq), u8(xs),
                                               m, static_cast<const int32_t*>(off.const_data_ptr()), index,
-                                              y.data_ptr(), dtype_code(y.scalar_type()), Stream(a[9], dev).handle);
+                                              y.data_ptr(), dtype_code(y.scalar_type()), stream(dev));
     return st ? status(st) : THPVariable_Wrap(y);
   });
 }
