@@ -122,6 +122,16 @@ def _stream(stream, dev=None):
     return _raw_stream(torch.cuda.current_device() if dev is None else dev)
 
 
+def _empty(shape, dtype, like, stream):
+    """An output of a call on ``stream``, from that stream's part of the
+    allocator: a block of the current stream could still be in use by work
+    queued there."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=like.device)
+    with torch.cuda.stream(stream):
+        return torch.empty(shape, dtype=dtype, device=like.device)
+
+
 def _need(t, name, dtypes, shape=None, dev=None):
     """Checks a tensor argument; dev: the current device's index when the
     caller already has it (a small call's checks cost more than its kernel)."""
@@ -174,10 +184,10 @@ def w4_quantize_pack(w, codec=W4_DYADIC, *, scales=None, codebook=None, packed=N
     _need(w, "w", _U16)
     n, k = w.shape
     if packed is None:
-        packed = torch.empty((n, k // 2), dtype=torch.uint8, device=w.device)
+        packed = _empty((n, k // 2), torch.uint8, w, stream)
     _need(packed, "packed", (torch.uint8,), (n, k // 2))
     if codec == W4_DYADIC and scales is None:
-        scales = torch.empty((n, k // 64), dtype=torch.bfloat16, device=w.device)
+        scales = _empty((n, k // 64), torch.bfloat16, w, stream)
     _side_tables(codec, n, k, scales, codebook)
     _check(_lib.w4_quantize_pack(codec, n, k, _ptr(w), _ptr(packed), _ptr(scales),
                                  _ptr(codebook), _stream(stream)))
@@ -193,7 +203,7 @@ def w4_unpack_dequant(packed, codec=W4_DYADIC, *, scales=None, codebook=None, ou
     _side_tables(codec, n, k, scales, codebook)
     dt = torch.float16 if codec == W4_SIGNMAG8 else torch.bfloat16
     if out is None:
-        out = torch.empty((n, k), dtype=dt, device=packed.device)
+        out = _empty((n, k), dt, packed, stream)
     _need(out, "out", _U16, (n, k))
     _check(_lib.w4_unpack_dequant(codec, n, k, _ptr(packed), _ptr(scales), _ptr(codebook),
                                   _ptr(out), _stream(stream)))
@@ -210,11 +220,11 @@ def w4_quantize_dyadic5(w, widths=None, *, packed=None, msb=None, scales=None, s
     if widths is not None:
         _need(widths, "widths", (torch.uint8,), (n, k // 64))
     if packed is None:
-        packed = torch.empty((n, k // 2), dtype=torch.uint8, device=w.device)
+        packed = _empty((n, k // 2), torch.uint8, w, stream)
     if msb is None:
-        msb = torch.empty((n, k // 8), dtype=torch.uint8, device=w.device)
+        msb = _empty((n, k // 8), torch.uint8, w, stream)
     if scales is None:
-        scales = torch.empty((n, k // 64), dtype=torch.bfloat16, device=w.device)
+        scales = _empty((n, k // 64), torch.bfloat16, w, stream)
     _need(packed, "packed", (torch.uint8,), (n, k // 2))
     _need(msb, "msb", (torch.uint8,), (n, k // 8))
     _need(scales, "scales", _U16, (n, k // 64))
@@ -231,9 +241,9 @@ def w4_lut16_fit(w, iters=25, *, scales=None, codebook=None, stream=None):
     _need(w, "w", _U16)
     n, k = w.shape
     if scales is None:
-        scales = torch.empty((n, k // 64), dtype=torch.bfloat16, device=w.device)
+        scales = _empty((n, k // 64), torch.bfloat16, w, stream)
     if codebook is None:
-        codebook = torch.empty((n, k // 64, 16), dtype=torch.bfloat16, device=w.device)
+        codebook = _empty((n, k // 64, 16), torch.bfloat16, w, stream)
     _need(scales, "scales", _U16, (n, k // 64))
     _need(codebook, "codebook", _U16, (n, k // 64, 16))
     _check(_lib.w4_lut16_fit(n, k, _ptr(w), _ptr(scales), _ptr(codebook), iters,
@@ -248,7 +258,7 @@ def w4_signmag8_fit(w, iters=25, *, codebook=None, stream=None):
     _need(w, "w", _U16)
     n, k = w.shape
     if codebook is None:
-        codebook = torch.empty((n, k // 32, 8), dtype=torch.float16, device=w.device)
+        codebook = _empty((n, k // 32, 8), torch.float16, w, stream)
     _need(codebook, "codebook", _U16, (n, k // 32, 8))
     _check(_lib.w4_signmag8_fit(n, k, _ptr(w), _ptr(codebook), iters, _stream(stream)))
     return codebook
@@ -261,9 +271,9 @@ def w4_signmag8_fit_warm(w, iters=25, *, codebook=None, params=None, stream=None
     _need(w, "w", _U16)
     n, k = w.shape
     if codebook is None:
-        codebook = torch.empty((n, k // 32, 8), dtype=torch.float16, device=w.device)
+        codebook = _empty((n, k // 32, 8), torch.float16, w, stream)
     if params is None:
-        params = torch.empty((n, k // 32), dtype=torch.uint8, device=w.device)
+        params = _empty((n, k // 32), torch.uint8, w, stream)
     _need(codebook, "codebook", _U16, (n, k // 32, 8))
     _need(params, "params", (torch.uint8,), (n, k // 32))
     _check(_lib.w4_signmag8_fit_warm(n, k, _ptr(w), _ptr(codebook), _ptr(params), iters,
@@ -283,8 +293,7 @@ def _matmul(fn, packed, x, codec, scales, codebook, y, y_dtype, stream):
     m = x.shape[0]
     code = W4_BF16 if y_dtype == torch.bfloat16 else W4_F32
     if y is None:
-        y = torch.empty((m, n), dtype=torch.bfloat16 if code == W4_BF16 else torch.float32,
-                        device=packed.device)
+        y = _empty((m, n), torch.bfloat16 if code == W4_BF16 else torch.float32, packed, stream)
     _need(y, "y", (torch.float32,) if code == W4_F32 else _U16, (m, n), dev)
     _check(fn(codec, n, k, _ptr(packed), _ptr(scales), _ptr(codebook), _ptr(x), m, _ptr(y),
               code, _stream(stream, dev)))
@@ -298,7 +307,7 @@ def w4_lut16s_interleave(packed, scales, out=None, stream=None):
     n, k = packed.shape[0], 2 * packed.shape[1]
     _need(scales, "scales", _U16, (n, k // 64))
     if out is None:
-        out = torch.empty((n, k // 256 * IL_RECORD), dtype=torch.uint8, device=packed.device)
+        out = _empty((n, k // 256 * IL_RECORD), torch.uint8, packed, stream)
     _need(out, "out", (torch.uint8,), (n, k // 256 * IL_RECORD))
     _check(_lib.w4_lut16s_interleave(n, k, _ptr(packed), _ptr(scales), _ptr(out),
                                      _stream(stream)))
