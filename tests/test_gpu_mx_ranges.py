@@ -131,3 +131,52 @@ def test_stream_argument_runs_there(w4, tokens):
         _chain(w4, *a, stream=side)
         side.synchronize()
         assert torch.equal(a[9], want[0]) and torch.equal(a[10], want[1]), rep
+
+
+# ------------------------------------------------------------------ more than a launch holds
+def repeats(t, part):
+    """Every whole run of part's length in t equals part, and so does what is left."""
+    n = part.shape[0]
+    whole = t.shape[0] // n
+    runs = t[:whole * n].view((whole,) + tuple(part.shape))
+    return all(bool((runs[i:i + 64] == part).all()) for i in range(0, whole, 64)) and \
+        torch.equal(t[whole * n:], part[:t.shape[0] - whole * n])
+
+
+@pytest.mark.parametrize("residual", [False, True])
+def test_rmsnorm_more_rows_than_a_launch(w4, residual):
+    report("mx_rmsnorm_rows", residual=residual)
+    g = torch.Generator("cuda").manual_seed(2)
+    base = torch.randn(4096, 32, generator=g, device="cuda").bfloat16()
+    gm = torch.rand(32, generator=g, device="cuda").bfloat16()
+    rows = 2 ** 24 + 1                               # 256 threads each: 2^32 and 256 more
+    x = torch.empty((rows, 32), dtype=torch.bfloat16, device="cuda")
+    x[:-1].view(-1, 4096, 32).copy_(base)
+    x[-1] = base[0]
+    y, yb = torch.zeros_like(x), torch.empty_like(base)
+    r, rb = (x, base) if residual else (None, None)
+    qb, sb, rob = w4.w4_mx_rmsnorm(base, gm, residual=rb, y=yb)
+    q, s, ro = w4.w4_mx_rmsnorm(x, gm, residual=r, y=y)
+    assert repeats(q, qb) and repeats(s, sb) and repeats(y, yb)
+    assert not residual or repeats(ro, rob)
+    del x, y, q, s, ro
+
+
+def test_quantize_and_rebuild_more_than_a_launch(w4):
+    report("mx_quantize_blocks")
+    rows, k = 2 ** 23 + 1, 4096                      # 2^24 and 2 blocks of 2048 values
+    if torch.cuda.mem_get_info()[0] < 100 << 30:
+        pytest.skip("needs 100 GiB of GPU memory")
+    g = torch.Generator("cuda").manual_seed(3)
+    base = torch.randn(4096, k, generator=g, device="cuda").bfloat16()
+    x = torch.empty((rows, k), dtype=torch.bfloat16, device="cuda")
+    x[:-1].view(-1, 4096, k).copy_(base)
+    x[-1] = base[0]
+    qb, sb = w4.w4_mx_quantize(base)
+    q, s = w4.w4_mx_quantize(x)
+    assert repeats(q, qb) and repeats(s, sb)
+    x.zero_()
+    w4.w4_mx_dequant(q, s, out=x)
+    assert repeats(x, w4.w4_mx_dequant(qb, sb))
+    del x, q, s
+    torch.cuda.empty_cache()

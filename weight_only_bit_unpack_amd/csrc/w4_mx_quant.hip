@@ -10,6 +10,8 @@
 // from the 256 MB cache), the rebuild to bf16 17.6 us; MXFP8 8192 x 4096 rebuilt
 // 16.2 us (102 MB, 6.3 TB/s); the norm with its residual, 8192 x 4096 bf16 to
 // MXFP8, 47.6 us (236 MB, 5.0 TB/s), one row of 2048 2.4 us.
+#include <type_traits>
+
 #include "w4_launch.h"
 #include "w4_mx_device.h"
 
@@ -142,45 +144,75 @@ hipError_t by_dtype(int dt, F&& f) {
                      : f(std::integral_constant<int, kF16>{});
 }
 
+// A launch holds fewer than 2^32 threads: arrays of more than 2^31 groups of
+// eight values, and norms of more than 2^23 rows, take several, each on its part.
+constexpr int64_t kMaxGroups = INT64_C(1) << 31;
+constexpr int64_t kMaxRows = INT64_C(1) << 23;
+
+constexpr int64_t mx_bytes(int fmt, int64_t values) { return fmt == kMxFp4 ? values / 2 : values; }
+constexpr int64_t dtype_bytes(int dtype, int64_t values) { return values * (dtype == kF32 ? 4 : 2); }
+
+template <typename P>
+P* ahead(P* p, int64_t bytes) {
+  using Byte = std::conditional_t<std::is_const_v<P>, const uint8_t, uint8_t>;
+  return p ? reinterpret_cast<P*>(reinterpret_cast<Byte*>(p) + bytes) : p;
+}
+
+// f(first, count) over parts of at most `most` of `total`, until one fails
+template <typename F>
+hipError_t in_parts(int64_t total, int64_t most, F&& f) {
+  hipError_t e = hipSuccess;
+  for (int64_t at = 0; at < total && e == hipSuccess; at += most) e = f(at, total - at < most ? total - at : most);
+  return e;
+}
+
 }  // namespace
 
 hipError_t launch_mx_quantize(int fmt, int64_t rows, int64_t k, const void* x, int dtype, uint8_t* q,
                               uint8_t* scales, hipStream_t stream) {
-  const int64_t total = rows * (k / 8);
-  const dim3 grid((uint32_t)((total + 255) / 256));
-  return by_format(fmt, [&](auto F) {
-    return by_dtype(dtype, [&](auto D) {
-      mx_quantize_kernel<decltype(F)::value, decltype(D)::value>
-          <<<grid, dim3(256), 0, stream>>>(x, q, scales, total);
-      return hipGetLastError();
+  return in_parts(rows * (k / 8), kMaxGroups, [&](int64_t at, int64_t n) {
+    const dim3 grid((uint32_t)((n + 255) / 256));
+    const void* const xp = ahead(x, dtype_bytes(dtype, 8 * at));
+    uint8_t* const qp = ahead(q, mx_bytes(fmt, 8 * at));
+    uint8_t* const sp = scales + at / 4;
+    return by_format(fmt, [&](auto F) {
+      return by_dtype(dtype, [&](auto D) {
+        mx_quantize_kernel<decltype(F)::value, decltype(D)::value><<<grid, dim3(256), 0, stream>>>(xp, qp, sp, n);
+        return hipGetLastError();
+      });
     });
   });
 }
 
 hipError_t launch_mx_dequant(int fmt, int64_t rows, int64_t k, const uint8_t* q, const uint8_t* scales,
                              void* out, int dtype, hipStream_t stream) {
-  const int64_t total = rows * (k / 8);
-  const dim3 grid((uint32_t)((total + 255) / 256));
-  return by_format(fmt, [&](auto F) {
-    auto go = [&](auto D) {
-      mx_dequant_kernel<decltype(F)::value, decltype(D)::value>
-          <<<grid, dim3(256), 0, stream>>>(q, scales, out, total);
-      return hipGetLastError();
-    };
-    return dtype == kF32 ? go(std::integral_constant<int, kF32>{})
-                         : go(std::integral_constant<int, kBf16>{});
+  return in_parts(rows * (k / 8), kMaxGroups, [&](int64_t at, int64_t n) {
+    const dim3 grid((uint32_t)((n + 255) / 256));
+    const uint8_t* const qp = ahead(q, mx_bytes(fmt, 8 * at));
+    const uint8_t* const sp = scales + at / 4;
+    void* const op = ahead(out, dtype_bytes(dtype, 8 * at));
+    return by_format(fmt, [&](auto F) {
+      auto go = [&](auto D) {
+        mx_dequant_kernel<decltype(F)::value, decltype(D)::value><<<grid, dim3(256), 0, stream>>>(qp, sp, op, n);
+        return hipGetLastError();
+      };
+      return dtype == kF32 ? go(std::integral_constant<int, kF32>{}) : go(std::integral_constant<int, kBf16>{});
+    });
   });
 }
 
 hipError_t launch_mx_rmsnorm(int fmt, int64_t rows, int64_t k, const void* x, const void* residual,
                              const void* gamma, int dtype, float eps, void* residual_out, void* y,
                              uint8_t* q, uint8_t* scales, hipStream_t stream) {
-  return by_format(fmt, [&](auto F) {
-    return by_dtype(dtype, [&](auto D) {
-      mx_rmsnorm_kernel<decltype(F)::value, decltype(D)::value>
-          <<<dim3((uint32_t)rows), dim3(256), 0, stream>>>(x, residual, gamma, residual_out, y, q,
-                                                           scales, k, eps);
-      return hipGetLastError();
+  return in_parts(rows, kMaxRows, [&](int64_t at, int64_t n) {
+    const int64_t b = dtype_bytes(dtype, at * k);
+    return by_format(fmt, [&](auto F) {
+      return by_dtype(dtype, [&](auto D) {
+        mx_rmsnorm_kernel<decltype(F)::value, decltype(D)::value><<<dim3((uint32_t)n), dim3(256), 0, stream>>>(
+            ahead(x, b), ahead(residual, b), gamma, ahead(residual_out, b), ahead(y, b),
+            ahead(q, mx_bytes(fmt, at * k)), ahead(scales, at * (k / 32)), k, eps);
+        return hipGetLastError();
+      });
     });
   });
 }
