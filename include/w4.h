@@ -518,7 +518,7 @@ w4_status w4_mx_rmsnorm(int32_t format, int64_t rows, int64_t k, const void* x,
  * w, w_scales, x, x_scales 16-byte aligned.
  * Errors: W4_EINVAL (bad format, negative size, null pointer), W4_ESHAPE
  * (k % 32 != 0, k above W4_MAX_MATMUL_K, n above W4_MAX_MX_N, m above
- * 2^31 - 1, too many tiles), W4_EALIGN, W4_EUNSUPPORTED (y_dtype), W4_EHIP.
+ * 2^31 - 1, more tiles than 2^32 threads work on), W4_EALIGN, W4_EUNSUPPORTED (y_dtype), W4_EHIP.
  * Workspace: with m > 16 and few output tiles the call may split k into S <= 8
  * parts and enqueue a second kernel that adds their fp32 sums in order; those
  * use S * m * n * 4 bytes that the library keeps per (device, stream) exactly

@@ -648,7 +648,7 @@ Plan make_plan(const MxProblem& p) {
         double us = full * (T::PER_CU == 2 ? pair : alone);
         if (rest) us += rest <= cus ? alone : pair;
         if (s > 1) us += 3.0 + (double)s * p.m * p.n * 8 / 4e6;
-        if (q.tiles_m * q.tiles_n * s > 0x7FFFFFF0) continue;
+        if ((q.tiles_m * q.tiles_n * s + 7) * T::THREADS > kMaxLaunchThreads) continue;
         if (best.tiles_m == 0 || us < least) {
           least = us;
           best = q;

@@ -148,6 +148,7 @@ hipError_t by_dtype(int dt, F&& f) {
 // eight values, and norms of more than 2^23 rows, take several, each on its part.
 constexpr int64_t kMaxGroups = INT64_C(1) << 31;
 constexpr int64_t kMaxRows = INT64_C(1) << 23;
+static_assert(kMaxGroups <= kMaxLaunchThreads && kMaxRows * 256 <= kMaxLaunchThreads);
 
 constexpr int64_t mx_bytes(int fmt, int64_t values) { return fmt == kMxFp4 ? values / 2 : values; }
 constexpr int64_t dtype_bytes(int dtype, int64_t values) { return values * (dtype == kF32 ? 4 : 2); }

@@ -264,7 +264,9 @@ bool few_rows(int x_fmt, const MxProblem& p) { return p.m <= (x_fmt == kMxFp8 ? 
 
 int64_t mx_skinny_blocks(int x_fmt, const MxProblem& p) {
   return by_shape(row_tiles(p) * ((p.n + 15) / 16), few_rows(x_fmt, p), [&](auto S) {
-    return row_tiles(p) * ((p.n + decltype(S)::BN - 1) / decltype(S)::BN);
+    using T = decltype(S);
+    const int64_t blocks = row_tiles(p) * ((p.n + T::BN - 1) / T::BN);
+    return blocks * (T::KS * T::WN * 64) > kMaxLaunchThreads ? INT64_C(1) << 31 : blocks;
   });
 }
 
