@@ -151,22 +151,26 @@ __global__ __launch_bounds__(256) void dequant_dyadic5_kernel(const uint32_t* __
 hipError_t launch_dequant(int codec, int64_t n, int64_t k, const uint8_t* packed,
                           const uint16_t* scales, const uint16_t* codebook, void* out,
                           hipStream_t stream) {
-  const int64_t ndw = n * k / 8;                 // packed dwords = 16-byte output chunks
-  const int64_t blocks = (ndw + 1023) / 1024;   // 4 waves x 256 dwords
-  const auto* pk = reinterpret_cast<const uint32_t*>(packed);
-  auto* o = reinterpret_cast<u32x4*>(out);
-  if (codec == 0)
-    dequant_dyadic_kernel<<<dim3((uint32_t)blocks), dim3(256), 0, stream>>>(pk, scales, o, ndw);
-  else if (codec == 1 || codec == 3)
-    dequant_lut16_kernel<<<dim3((uint32_t)blocks), dim3(256), 0, stream>>>(
-        pk, scales, reinterpret_cast<const u32x4*>(codebook), o, ndw, codec == 3);
-  else if (codec == 4)
-    dequant_dyadic5_kernel<<<dim3((uint32_t)blocks), dim3(256), 0, stream>>>(
-        pk, reinterpret_cast<const uint32_t*>(codebook), scales, o, ndw);
-  else
-    dequant_signmag8_kernel<<<dim3((uint32_t)blocks), dim3(256), 0, stream>>>(
-        pk, reinterpret_cast<const u32x4*>(codebook), o, ndw);
-  return hipGetLastError();
+  return in_parts(n * k, kMaxLaunchWeights, [&](int64_t at, int64_t count) {
+    const int64_t ndw = count / 8;                            // packed dwords = 16-byte output chunks
+    const dim3 grid((uint32_t)((ndw + 1023) / 1024));         // 4 waves x 256 dwords
+    const auto* pk = reinterpret_cast<const uint32_t*>(packed + at / 2);
+    auto* o = reinterpret_cast<u32x4*>(reinterpret_cast<uint16_t*>(out) + at);
+    if (codec == 0)
+      dequant_dyadic_kernel<<<grid, dim3(256), 0, stream>>>(pk, scales + at / 64, o, ndw);
+    else if (codec == 1 || codec == 3)
+      dequant_lut16_kernel<<<grid, dim3(256), 0, stream>>>(
+          pk, scales + at / 64, reinterpret_cast<const u32x4*>(codec == 3 ? codebook : codebook + at / 64 * 16), o, ndw,
+          codec == 3);
+    else if (codec == 4)
+      // (the high-bit plane: a 32-bit word per 32 weights)
+      dequant_dyadic5_kernel<<<grid, dim3(256), 0, stream>>>(
+          pk, reinterpret_cast<const uint32_t*>(codebook) + at / 32, scales + at / 64, o, ndw);
+    else
+      dequant_signmag8_kernel<<<grid, dim3(256), 0, stream>>>(
+          pk, reinterpret_cast<const u32x4*>(codebook + at / 32 * 8), o, ndw);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace w4

@@ -422,33 +422,40 @@ __global__ __launch_bounds__(256) void warm_fit_kernel(const uint16_t* __restric
 
 }  // namespace
 
+// Groups are independent and lie one after another, so a fit takes them as rows
+// of one group, in parts of at most 2^23 blocks.
+constexpr int64_t kMaxLaunchBlocks = INT64_C(1) << 23;
+static_assert(kMaxLaunchBlocks * 256 <= kMaxLaunchThreads);
+
 hipError_t launch_lut16_fit(int64_t n, int64_t k, const uint16_t* w, uint16_t* scales,
                             uint16_t* lut, int iters, hipStream_t stream) {
-  const int64_t groups = n * (k / 64), per_block = 16;
-  const int64_t blocks = (groups + per_block - 1) / per_block;
-  lloyd_fit_kernel<16, false>
-      <<<dim3((uint32_t)blocks), dim3(256), 0, stream>>>(w, n, k, iters, scales, lut);
-  return hipGetLastError();
+  constexpr int64_t per_block = 16;
+  return in_parts(n * (k / 64), kMaxLaunchBlocks * per_block, [&](int64_t at, int64_t groups) {
+    lloyd_fit_kernel<16, false><<<dim3((uint32_t)((groups + per_block - 1) / per_block)), dim3(256), 0, stream>>>(
+        w + at * 64, groups, 64, iters, scales + at, lut + at * 16);
+    return hipGetLastError();
+  });
 }
 
 hipError_t launch_signmag8_fit(int64_t n, int64_t k, const uint16_t* w, uint16_t* codebook,
                                int iters, hipStream_t stream) {
-  const int64_t groups = n * (k / 32), per_block = 32;
-  const int64_t blocks = (groups + per_block - 1) / per_block;
-  lloyd_fit_kernel<8, true>
-      <<<dim3((uint32_t)blocks), dim3(256), 0, stream>>>(w, n, k, iters, nullptr, codebook);
-  return hipGetLastError();
+  constexpr int64_t per_block = 32;
+  return in_parts(n * (k / 32), kMaxLaunchBlocks * per_block, [&](int64_t at, int64_t groups) {
+    lloyd_fit_kernel<8, true><<<dim3((uint32_t)((groups + per_block - 1) / per_block)), dim3(256), 0, stream>>>(
+        w + at * 32, groups, 32, iters, nullptr, codebook + at * 8);
+    return hipGetLastError();
+  });
 }
 
 hipError_t launch_signmag8_warm_fit(int64_t n, int64_t k, const uint16_t* w, uint16_t* codebook,
                                     uint8_t* params, int iters, hipStream_t stream) {
   BrelRat brel;
   for (int i = 0; i < 15; ++i) brel.v[i] = std::pow(10.0, (double)(5 * i - 42) / 14.0);
-  const int64_t groups = n * (k / 32);
-  const int64_t blocks = (groups + kWarmGroups - 1) / kWarmGroups;
-  warm_fit_kernel<<<dim3((uint32_t)blocks), dim3(256), 0, stream>>>(w, n, k, iters, brel,
-                                                                     codebook, params);
-  return hipGetLastError();
+  return in_parts(n * (k / 32), kMaxLaunchBlocks * kWarmGroups, [&](int64_t at, int64_t groups) {
+    warm_fit_kernel<<<dim3((uint32_t)((groups + kWarmGroups - 1) / kWarmGroups)), dim3(256), 0, stream>>>(
+        w + at * 32, groups, 32, iters, brel, codebook + at * 8, params ? params + at : nullptr);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace w4

@@ -8,6 +8,22 @@
 
 namespace w4 {
 
+// A launch holds fewer than 2^32 threads (HIP cuts a larger one without an error).
+constexpr int64_t kMaxLaunchThreads = 0xFFFFFFFF;
+
+// f(first, count) over parts of at most `most` of `total`, until one fails: the
+// launches of an elementwise call.
+template <typename F>
+hipError_t in_parts(int64_t total, int64_t most, F&& f) {
+  hipError_t e = hipSuccess;
+  for (int64_t at = 0; at < total && e == hipSuccess; at += most) e = f(at, total - at < most ? total - at : most);
+  return e;
+}
+
+// Weights of a launch of the codecs' elementwise kernels: a thread takes eight
+// at least.
+constexpr int64_t kMaxLaunchWeights = INT64_C(1) << 33;
+
 // Same layout as w4_gemv_problem in include/w4.h.
 struct GemvProblem {
   const uint8_t* packed;
@@ -97,8 +113,6 @@ hipError_t launch_mx_dequant(int fmt, int64_t rows, int64_t k, const uint8_t* q,
 hipError_t launch_mx_rmsnorm(int fmt, int64_t rows, int64_t k, const void* x, const void* residual,
                              const void* gamma, int dtype, float eps, void* residual_out, void* y,
                              uint8_t* q, uint8_t* scales, hipStream_t stream);
-// A launch holds fewer than 2^32 threads (HIP cuts a larger one without an error).
-constexpr int64_t kMaxLaunchThreads = 0xFFFFFFFF;
 // blocks of the product's launch; 2^31 or more: too many for a launch
 int64_t mx_linear_blocks(int x_fmt, const MxProblem& p);
 hipError_t launch_mx_linear(int x_fmt, const MxProblem& p, hipStream_t stream);

@@ -159,14 +159,6 @@ P* ahead(P* p, int64_t bytes) {
   return p ? reinterpret_cast<P*>(reinterpret_cast<Byte*>(p) + bytes) : p;
 }
 
-// f(first, count) over parts of at most `most` of `total`, until one fails
-template <typename F>
-hipError_t in_parts(int64_t total, int64_t most, F&& f) {
-  hipError_t e = hipSuccess;
-  for (int64_t at = 0; at < total && e == hipSuccess; at += most) e = f(at, total - at < most ? total - at : most);
-  return e;
-}
-
 }  // namespace
 
 hipError_t launch_mx_quantize(int fmt, int64_t rows, int64_t k, const void* x, int dtype, uint8_t* q,

@@ -375,39 +375,44 @@ __global__ __launch_bounds__(256) void lut16s_interleave_kernel(const u32x4* __r
 
 hipError_t launch_lut16s_interleave(int64_t n, int64_t k, const uint8_t* packed,
                                     const uint16_t* scales, uint8_t* out, hipStream_t stream) {
-  const int64_t nchunks = n * (k / 256) * 9;
-  const int64_t blocks = (nchunks + 255) / 256;
-  lut16s_interleave_kernel<<<dim3((uint32_t)blocks), dim3(256), 0, stream>>>(
-      reinterpret_cast<const u32x4*>(packed), scales, reinterpret_cast<u32x4*>(out), nchunks);
-  return hipGetLastError();
+  return in_parts(n * (k / 256), kMaxLaunchWeights / 256, [&](int64_t at, int64_t records) {
+    const int64_t nchunks = records * 9;
+    lut16s_interleave_kernel<<<dim3((uint32_t)((nchunks + 255) / 256)), dim3(256), 0, stream>>>(
+        reinterpret_cast<const u32x4*>(packed + at * 128), scales + at * 4,
+        reinterpret_cast<u32x4*>(out + at * 144), nchunks);
+    return hipGetLastError();
+  });
 }
 
 hipError_t launch_quantize_dyadic5(int64_t n, int64_t k, const uint16_t* w, const uint8_t* widths,
                                    uint8_t* packed, uint8_t* msb, uint16_t* scales,
                                    hipStream_t stream) {
-  const int64_t nruns = n * k / 32;
-  const int64_t blocks = (nruns + 255) / 256;
-  quantize_dyadic5_kernel<<<dim3((uint32_t)blocks), dim3(256), 0, stream>>>(
-      reinterpret_cast<const u32x4*>(w), widths, reinterpret_cast<u32x4*>(packed),
-      reinterpret_cast<uint32_t*>(msb), scales, nruns);
-  return hipGetLastError();
+  return in_parts(n * k, kMaxLaunchWeights, [&](int64_t at, int64_t count) {
+    const int64_t nruns = count / 32;
+    quantize_dyadic5_kernel<<<dim3((uint32_t)((nruns + 255) / 256)), dim3(256), 0, stream>>>(
+        reinterpret_cast<const u32x4*>(w + at), widths ? widths + at / 64 : nullptr,
+        reinterpret_cast<u32x4*>(packed + at / 2), reinterpret_cast<uint32_t*>(msb + at / 8), scales + at / 64, nruns);
+    return hipGetLastError();
+  });
 }
 
 hipError_t launch_quantize(int codec, int64_t n, int64_t k, const uint16_t* w, uint8_t* packed,
                            uint16_t* scales, const uint16_t* codebook, hipStream_t stream) {
-  const int64_t nchunks = n * k / 8;
-  const int64_t blocks = (nchunks + 255) / 256;
-  const auto* wv = reinterpret_cast<const u32x4*>(w);
-  auto* pk = reinterpret_cast<uint32_t*>(packed);
-  if (codec == 0)
-    quantize_dyadic_kernel<<<dim3((uint32_t)blocks), dim3(256), 0, stream>>>(wv, pk, scales, nchunks);
-  else if (codec == 1 || codec == 3)
-    quantize_lut16_kernel<<<dim3((uint32_t)((nchunks / 8 + 255) / 256)), dim3(256), 0, stream>>>(
-        wv, pk, scales, reinterpret_cast<const u32x4*>(codebook), nchunks / 8, codec == 3);
-  else
-    quantize_signmag8_kernel<<<dim3((uint32_t)((nchunks / 4 + 255) / 256)), dim3(256), 0, stream>>>(
-        wv, pk, reinterpret_cast<const u32x4*>(codebook), nchunks / 4);
-  return hipGetLastError();
+  return in_parts(n * k, kMaxLaunchWeights, [&](int64_t at, int64_t count) {
+    const auto* wv = reinterpret_cast<const u32x4*>(w + at);
+    auto* pk = reinterpret_cast<uint32_t*>(packed + at / 2);
+    auto grid = [](int64_t threads) { return dim3((uint32_t)((threads + 255) / 256)); };
+    if (codec == 0)
+      quantize_dyadic_kernel<<<grid(count / 8), dim3(256), 0, stream>>>(wv, pk, scales + at / 64, count / 8);
+    else if (codec == 1 || codec == 3)
+      quantize_lut16_kernel<<<grid(count / 64), dim3(256), 0, stream>>>(
+          wv, pk, scales + at / 64, reinterpret_cast<const u32x4*>(codec == 3 ? codebook : codebook + at / 64 * 16),
+          count / 64, codec == 3);
+    else
+      quantize_signmag8_kernel<<<grid(count / 32), dim3(256), 0, stream>>>(
+          wv, pk, reinterpret_cast<const u32x4*>(codebook + at / 32 * 8), count / 32);
+    return hipGetLastError();
+  });
 }
 
 }  // namespace w4
