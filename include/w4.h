@@ -23,8 +23,8 @@
  *  - Pointers are DEVICE pointers owned by the caller, all on the current
  *    device (hipSetDevice), as is `stream`; the library keeps none of them
  *    after returning.  It allocates no memory, except w4_gemm and
- *    w4_gemv with m >= 2, which keep a device workspace per (device, stream)
- *    for the process's life (see there).
+ *    w4_gemv with m >= 2, which keep a device workspace per (device, stream;
+ *    hipStreamPerThread: per thread) for the process's life (see there).
  *  - `stream` is a hipStream_t (NULL = the null stream).  A call only enqueues
  *    work on it; it never synchronises the stream or the device.
  *  - All validation happens on the host before anything is enqueued.  On any
