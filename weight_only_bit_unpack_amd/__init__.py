@@ -6,7 +6,8 @@ forwards raw device pointers and the current HIP stream to the C ABI
 (``include/w4.h``), whose functions carry the same names.  All computation
 happens in the HIP kernels; there is no fallback of any kind, and importing
 this package fails if ``libw4.so`` has not been built
-(``python weight_only_bit_unpack_amd/build.py``).
+(``python weight_only_bit_unpack_amd/build.py``); the MX operators' calls fail if
+their binding ``_w4mx.so`` has not been built for this torch.
 """
 
 import ctypes
@@ -30,7 +31,26 @@ if not os.path.exists(LIB_PATH):
         f"{LIB_PATH} is missing: build it with `python weight_only_bit_unpack_amd/build.py`")
 
 _lib = ctypes.CDLL(LIB_PATH)
-from . import _w4mx  # noqa: E402  (links libw4.so; built with it)
+
+
+class _MissingMx:
+    """In the place of _w4mx where it does not load: the codecs need only libw4.so
+    and work without it."""
+
+    def __init__(self, error):
+        self._error = error
+
+    def __getattr__(self, name):
+        raise ImportError(
+            f"the MX operators need {os.path.join(_HERE, '_w4mx.so')}, which does not load: build it "
+            "for this torch with `python weight_only_bit_unpack_amd/build.py`") from self._error
+
+
+try:
+    from . import _w4mx  # (links libw4.so)
+except ImportError as _error:
+    _w4mx = _MissingMx(_error)
+
 _P, _I32, _I64 = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64
 
 
@@ -398,8 +418,9 @@ def w4_gemv_batched_plan(problems, codec=W4_DYADIC, y_dtype=torch.float32):
 _MX_DTYPE = {torch.float32: W4_F32, torch.bfloat16: W4_BF16, torch.float16: W4_F16}
 
 
-_w4mx.set_stream_query(
-    _raw_stream or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
+if not isinstance(_w4mx, _MissingMx):
+    _w4mx.set_stream_query(
+        _raw_stream or (lambda dev: torch.cuda.current_stream(dev).cuda_stream))
 
 
 def _mx(stream, call, *args):
