@@ -83,7 +83,10 @@ struct GemmArgs {
 // `to` (the same in every lane), without registers between.  Written as
 // assembly because after the builtin form the compiler makes every LDS read
 // wait for all copies in flight, the next step's too; the waits are placed by
-// hand instead.  It has no register outputs.
+// hand instead.  It has no register outputs.  It writes m0, which this compiler
+// reserves and does not let a statement declare as written: in these kernels
+// nothing else may read or set m0 (no builtin that moves to or from LDS or
+// indexes registers through it; the assembly holds no other use).
 __device__ __forceinline__ uint32_t lds_address(const u32x4* p) {
   return __builtin_amdgcn_readfirstlane(
       (uint32_t)(uintptr_t)(const __attribute__((address_space(3))) void*)p);
