@@ -1,0 +1,252 @@
+"""Every kernel of the MX products by name, each at the sizes where its loop, its
+tile and its groups end, whatever the rule that chooses between them takes.
+
+The operands are small whole numbers times powers of two, so that every product
+is a whole number of at most 3 * 4 * 3 * 2 = 72 and every sum of them below 2^24:
+the matrix core's sums are exact with either format (with MXFP8 it drops bits
+below 2^-13 of the largest of a few products, here 72 * 2^-13 < 1), and outputs
+are compared bit for bit, bf16 ones after the one rounding.
+"""
+
+import ctypes
+
+import numpy as np
+import pytest
+import torch
+
+from tests.gpu_util import report
+from tests.test_gpu_mx import FMTS, canary, code, edges_kept
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = torch.float32, torch.bfloat16
+TILE = {"fp8": [(128, 256), (128, 128), (64, 256), (64, 128), (64, 128)],     # rows of x, of the weight
+        "fp4": [(256, 256), (128, 256), (128, 128), (64, 256), (64, 128)]}
+WHOLE = {"fp4": [0, 2, 4, 5], "fp8": [0, 0x38, 0x40, 0x44]}                    # codes of 0, 1, 2, 3
+SIGN = {"fp4": 8, "fp8": 128}
+# around the step counts at which the loops change: 256 of k a step, scales copied
+# two steps at a time, two to four steps in flight, and ends inside a step
+STEPS = [256 * s + d for s in (1, 2, 3, 4, 5, 6, 7, 9) for d in (-224, -96, -32, 0, 32, 128)]
+
+
+@pytest.fixture(scope="module")
+def w4():
+    import weight_only_bit_unpack_amd as m
+    i32, i64, p = ctypes.c_int32, ctypes.c_int64, ctypes.c_void_p
+    f = m._lib.w4_mx_product_on
+    f.argtypes, f.restype = [i32, i32, i32, i64, i64, p, p, i64, p, p, i64, p, p, p, i32, p], i32
+    return m
+
+
+def operand(g, shape, k, fmt, scales):
+    """Bytes, scale bytes and fp64 values of a random operand [*shape, k]."""
+    v = torch.randint(0, 4, shape + (k,), generator=g, device="cuda")
+    neg = torch.randint(0, 2, shape + (k,), generator=g, device="cuda")
+    c = torch.tensor(WHOLE[fmt], device="cuda")[v] + neg * SIGN[fmt]
+    s = torch.randint(127, 127 + scales, shape + (k // 32,), generator=g, device="cuda")
+    q = (c[..., 0::2] | c[..., 1::2] << 4) if fmt == "fp4" else c
+    val = (v * (1 - 2 * neg)).double() * torch.exp2((s - 127).double()).repeat_interleave(32, -1)
+    return q.to(torch.uint8), s.to(torch.uint8), val
+
+
+def run(w4, kernel, fmt, x, w, y, off=None, idx=None):
+    """The product of x and w (bytes, scales, ...) on the kernel, into y."""
+    experts = 0 if off is None else w[0].shape[0]
+    at = lambda t: None if t is None else t.data_ptr()
+    e = w4._lib.w4_mx_product_on(kernel, code(w4, fmt), experts, w[0].shape[-2], 2 * w[0].shape[-1], at(w[0]), at(w[1]),
+                                 x[0].shape[0], at(x[0]), at(x[1]), y.shape[0], at(off), at(idx), at(y),
+                                 int(y.dtype == BF16), torch.cuda.current_stream().cuda_stream)
+    assert e == 0, e
+
+
+def equal(y, want):
+    """The same values bit for bit, NaN in the same places (zeros of either sign)."""
+    want = want.to(y.dtype)
+    return torch.equal(torch.isnan(y), torch.isnan(want)) and torch.equal(torch.nan_to_num(y), torch.nan_to_num(want))
+
+
+def exact(x, w):
+    """The product in fp64 (the right operand as a plain matrix)."""
+    return x @ w.t().contiguous()
+
+
+def check(w4, kernel, fmt, x, w, dtype, off=None, idx=None, want=None):
+    m, n = want.shape
+    buf, y = canary(m, n, dtype)
+    run(w4, kernel, fmt, x, w, y, off, idx)
+    assert equal(y, want)
+    assert edges_kept(buf, m, n)
+
+
+KERNELS = [(fmt, t) for fmt in FMTS for t in range(5)]
+
+
+@pytest.mark.parametrize("fmt,t", KERNELS)
+def test_tile_step_counts(w4, fmt, t):
+    """Every count of steps and every end of k, on whole tiles and ragged ones."""
+    g = torch.Generator("cuda").manual_seed(t)
+    bm, bn = TILE[fmt][t]
+    for i, k in enumerate(STEPS):
+        m, n = [(bm, bn), (2 * bm + 17, bn + 34), (bm - 31, 2 * bn + 1)][i % 3]
+        report("mx_tile_steps", fmt=fmt, tile=t, m=m, n=n, k=k)
+        x, w = operand(g, (m,), k, fmt, 3), operand(g, (n,), k, "fp4", 2)
+        want = exact(x[2], w[2])
+        for dtype in (F32, BF16):
+            check(w4, 16 + t, fmt, x, w, dtype, want=want)
+
+
+@pytest.mark.parametrize("parts", [2, 4, 8])
+@pytest.mark.parametrize("fmt,t", KERNELS)
+def test_tile_split_k(w4, fmt, t, parts):
+    """Parts of k: as few steps as a part has, uneven parts, and ends inside a step."""
+    g = torch.Generator("cuda").manual_seed(10 + t)
+    bm, bn = TILE[fmt][t]
+    for i, k in enumerate([256 * s + d for s in (2 * parts, 2 * parts + 1, 3 * parts, 5 * parts + 3)
+                           for d in (-96, 0, 64)]):
+        if (k + 255) // 256 < 2 * parts:
+            continue
+        m, n = [(bm + 1, bn + 2), (17, bn - 3), (2 * bm, 30)][i % 3]
+        report("mx_tile_split", fmt=fmt, tile=t, parts=parts, m=m, n=n, k=k)
+        x, w = operand(g, (m,), k, fmt, 3), operand(g, (n,), k, "fp4", 2)
+        want = exact(x[2], w[2])
+        for dtype in (F32, BF16):
+            check(w4, 16 * parts + t, fmt, x, w, dtype, want=want)
+
+
+def grouped_want(x, w, ends, idx, rows):
+    """fp64 rows of a grouped product; ends: of each expert's rows."""
+    want = torch.zeros((rows, w.shape[1]), dtype=torch.float64, device="cuda")
+    src = torch.arange(rows, device="cuda") if idx is None else idx.long()
+    ok = (src >= 0) & (src < x.shape[0])
+    xs = torch.where(ok[:, None], x[src.clamp(0, x.shape[0] - 1)], 0.0)
+    lo = 0
+    for e, hi in enumerate(ends):
+        if hi > lo:
+            want[lo:hi] = exact(xs[lo:hi], w[e])
+        lo = hi
+    return torch.where(ok[:, None], want, 0.0)               # (also where x is NaN)
+
+
+def grouped_case(g, fmt, bm, n, k, gather, spare):
+    """Groups of no rows, one row, around a tile's rows and several tiles."""
+    counts = [bm, 0, 1, bm + 1, 0, 2 * bm - 1, 33, bm // 2, 0]
+    ends = np.cumsum(counts).tolist()
+    rows = ends[-1] + spare
+    tokens = 77 if gather else rows
+    x, w = operand(g, (tokens,), k, fmt, 3), operand(g, (len(counts), n), k, "fp4", 2)
+    idx = None
+    if gather:
+        idx = torch.randint(0, tokens, (rows,), generator=g, device="cuda").to(torch.int32)
+        for i, v in enumerate((-1, tokens, 2 ** 31 - 1, -2 ** 31)):
+            idx[(i * 37 + 5) % rows::131] = v
+    off = torch.tensor([0] + ends, dtype=torch.int32, device="cuda")
+    return x, w, off, idx, grouped_want(x[2], w[2], ends, idx, rows)
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("fmt,t", KERNELS)
+def test_tile_grouped(w4, fmt, t, gather):
+    """Ragged groups, idle experts, spare rows and indices outside x."""
+    g = torch.Generator("cuda").manual_seed(20 + t)
+    bm, bn = TILE[fmt][t]
+    for i, k in enumerate(STEPS[3::4] + [512, 1024, 2048]):
+        n = [bn, bn + 34, 2 * bn + 1][i % 3]
+        report("mx_tile_grouped", fmt=fmt, tile=t, gather=gather, n=n, k=k)
+        x, w, off, idx, want = grouped_case(g, fmt, bm, n, k, gather, [0, 1, bm + 9][i % 3])
+        for dtype in (F32, BF16):
+            check(w4, 16 + t, fmt, x, w, dtype, off, idx, want)
+
+
+@pytest.mark.parametrize("shape", [0, 1, 2])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_few_rows(w4, fmt, shape):
+    """The few-row kernel's shapes: rows of x to 16, ragged columns, every end of k."""
+    g = torch.Generator("cuda").manual_seed(30 + shape)
+    for i, k in enumerate(STEPS + [32, 64, 96, 128, 4096, 8192 + 32]):
+        m = [1, 2, 4, 5, 8, 9, 15, 16][i % 8]
+        n = [16, 1, 130, 64, 127, 257, 33][i % 7]
+        report("mx_few_rows", fmt=fmt, shape=shape, m=m, n=n, k=k)
+        x, w = operand(g, (m,), k, fmt, 3), operand(g, (n,), k, "fp4", 2)
+        want = exact(x[2], w[2])
+        for dtype in (F32, BF16):
+            check(w4, 256 + shape, fmt, x, w, dtype, want=want)
+
+
+@pytest.mark.parametrize("shape", [0, 1, 2])
+@pytest.mark.parametrize("fmt", FMTS)
+def test_few_rows_grouped(w4, fmt, shape):
+    g = torch.Generator("cuda").manual_seed(40 + shape)
+    for i, k in enumerate(STEPS[1::3] + [32, 2048]):
+        n = [64, 130, 257][i % 3]
+        report("mx_few_rows_grouped", fmt=fmt, shape=shape, n=n, k=k)
+        for gather in (False, True):
+            x, w, off, idx, want = grouped_case(g, fmt, 16, n, k, gather, [0, 1, 25][i % 3])
+            for dtype in (F32, BF16):
+                check(w4, 256 + shape, fmt, x, w, dtype, off, idx, want)
+        # four rows of y and fewer take one load instruction of x a step
+        for rows in (1, 3):
+            x, w = operand(g, (rows,), k, fmt, 3), operand(g, (5, n), k, "fp4", 2)
+            ends = [0, rows - 1, rows - 1, rows, rows]
+            off = torch.tensor([0] + ends, dtype=torch.int32, device="cuda")
+            check(w4, 256 + shape, fmt, x, w, F32, off, None, grouped_want(x[2], w[2], ends, None, rows))
+
+
+ALL = [(fmt, 16 + t) for fmt in FMTS for t in range(5)] + [(fmt, 32 + t) for fmt in FMTS for t in range(5)] + \
+    [(fmt, 256 + s) for fmt in FMTS for s in range(3)]
+
+
+@pytest.mark.parametrize("fmt,kernel", ALL)
+def test_nan_and_scale_range(w4, fmt, kernel):
+    """NaN scales and elements make their own rows and columns NaN and nothing else,
+    at either end of k; scales far from one cancel."""
+    g = torch.Generator("cuda").manual_seed(kernel)
+    bm, bn = (16, 64) if kernel >= 256 else TILE[fmt][kernel % 16]
+    m, n = (16 if kernel >= 256 else bm + 20), bn + 10
+    for k in (1024, 1120, 1184, 2048):
+        report("mx_nan", fmt=fmt, kernel=kernel, m=m, n=n, k=k)
+        x, w = operand(g, (m,), k, fmt, 3), operand(g, (n,), k, "fp4", 2)
+        want = exact(x[2], w[2])
+        check(w4, kernel, fmt, (x[0], x[1] + 100), (w[0], w[1] - 100), F32, want=want)
+        xq, xs, ws, bad = x[0].clone(), x[1].clone(), w[1].clone(), torch.zeros_like(want)
+        ws[3, k // 32 - 1], ws[n - 1, 0], ws[5, 11] = 255, 255, 255
+        xs[m - 1, 0], xs[1, k // 32 - 1], xs[0, 13] = 255, 255, 255
+        bad[:, [3, 5, n - 1]] = float("nan")
+        bad[[0, 1, m - 1]] = float("nan")
+        if fmt == "fp8":
+            xq[4, k - 1], xq[6, 0], xq[9, 300] = 0x7F, 0xFF, 0x7F
+            bad[[4, 6, 9]] = float("nan")
+        check(w4, kernel, fmt, (xq, xs), (w[0], ws), F32, want=want + bad)
+
+
+@pytest.mark.parametrize("fmt,kernel", [a for a in ALL if not 32 <= a[1] < 48])
+def test_nan_stays_in_its_group(w4, fmt, kernel):
+    """A NaN row of x or a NaN weight of one expert reaches only the rows that use it,
+    not those of another expert, of no expert or with an index outside x."""
+    g = torch.Generator("cuda").manual_seed(kernel)
+    bm, bn = (16, 64) if kernel >= 256 else TILE[fmt][kernel % 16]
+    n = bn + 10
+    for k in (544, 1024):
+        report("mx_nan_grouped", fmt=fmt, kernel=kernel, n=n, k=k)
+        x, w, off, idx, _ = grouped_case(g, fmt, bm, n, k, True, 21)
+        xs, ws, xv, wv = x[1].clone(), w[1].clone(), x[2].clone(), w[2].clone()
+        xs[0, k // 32 - 1], ws[3, 7, 0] = 255, 255             # (row 0: what a bad index reads)
+        xv[0], wv[3, 7] = float("nan"), float("nan")
+        want = grouped_want(xv, wv, off[1:].tolist(), idx, idx.shape[0])
+        check(w4, kernel, fmt, (x[0], xs), (w[0], ws), F32, off, idx, want)
+
+
+def test_kernels_that_do_not_fit_are_refused(w4):
+    """Before any launch: parts of fewer than two steps, split groups, rows past a
+    few-row tile, and kernels that there are not."""
+    report("mx_kernel_refusals")
+    g = torch.Generator("cuda").manual_seed(50)
+    x, w = operand(g, (17,), 512, "fp8", 3), operand(g, (1, 32), 512, "fp4", 2)
+    off = torch.tensor([0, 17], dtype=torch.int32, device="cuda")
+    y = torch.zeros((17, 32), device="cuda")
+    one = (w[0][0], w[1][0])
+    for kernel, weight, o in ((32, one, None), (64, one, None), (256, one, None), (259, one, None), (5, one, None),
+                              (16 + 5, one, None), (16 * 9, one, None), (32, w, off)):
+        with pytest.raises(AssertionError):
+            run(w4, kernel, "fp8", x, weight, y, o)
+    torch.cuda.synchronize()
+    assert bool((y == 0).all())

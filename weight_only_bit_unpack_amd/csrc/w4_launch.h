@@ -116,8 +116,20 @@ hipError_t launch_mx_rmsnorm(int fmt, int64_t rows, int64_t k, const void* x, co
 // blocks of the product's launch; 2^31 or more: too many for a launch
 int64_t mx_linear_blocks(int x_fmt, const MxProblem& p);
 hipError_t launch_mx_linear(int x_fmt, const MxProblem& p, hipStream_t stream);
+// For the tests, which name the kernel that they run: kernel 16 * parts of k +
+// tile (w4_mx_gemm.hip), or with few rows a weight 256 + shape (w4_mx_skinny.hip).
+// The kernel that a product takes (experts 0: one weight):
+extern "C" int32_t w4_mx_kernel_of(int32_t x_fmt, int32_t experts, int64_t n, int64_t k, int64_t m);
+// The product on a kernel of the caller's choice, with arguments that
+// w4_mx_grouped_linear accepts (offsets == nullptr: w4_mx_linear) and something
+// to compute; a hipError_t, an error where the kernel does not fit the product.
+extern "C" int32_t w4_mx_product_on(int32_t kernel, int32_t x_fmt, int32_t experts, int64_t n, int64_t k,
+                                    const uint8_t* w, const uint8_t* w_scales, int64_t tokens, const uint8_t* x,
+                                    const uint8_t* x_scales, int64_t rows, const int32_t* offsets,
+                                    const int32_t* row_index, void* y, int32_t y_bf16, void* stream);
 // few rows of x a weight (w4_mx_skinny.hip)
 int64_t mx_skinny_blocks(int x_fmt, const MxProblem& p);
-hipError_t launch_mx_skinny(int x_fmt, const MxProblem& p, hipStream_t stream);
+int mx_skinny_shape(int x_fmt, const MxProblem& p);  // 0 .. 2
+hipError_t launch_mx_skinny(int x_fmt, const MxProblem& p, int shape, hipStream_t stream);
 
 }  // namespace w4

@@ -619,6 +619,22 @@ struct Plan {
   int64_t blocks() const { return (tiles_m * tiles_n * splits + 7) / 8 * 8; }
 };
 
+// Groups that have rows, the rows of no expert among them, at most.
+int64_t most_groups(const MxProblem& p) { return p.m < p.experts + 1 ? p.m : p.experts + 1; }
+
+// Tile number t with k in s parts; tile < 0 where they do not fit the problem:
+// a tile of y stays below 2^31 bytes, grouped products do not split k, each part
+// has two steps of k, and a launch holds the blocks.
+template <typename T>
+Plan plan_on(const MxProblem& p, int t, uint32_t s) {
+  Plan q{t, s, (p.m + T::BM - 1) / T::BM, (p.n + T::BN - 1) / T::BN};
+  if (p.offsets) q.tiles_m = most_groups(p) + (p.m - most_groups(p)) / T::BM;
+  if (p.n > ((INT64_C(1) << 31) - 1) / 4 / T::BM) q.tile = -1;
+  if (s > 1 && (p.offsets || 2 * (int64_t)s > (p.k + 255) / 256)) q.tile = -1;
+  if ((q.tiles_m * q.tiles_n * s + 7) * T::THREADS > kMaxLaunchThreads) q.tile = -1;
+  return q;
+}
+
 // The tile and, for one weight, the parts of k that the costs above say take
 // the least time; the parts' sums cost a launch (3 us) and their bytes, written
 // and read, at 4 TB/s.  Examples (us, measured, the five tiles, each
@@ -634,16 +650,12 @@ Plan make_plan(const MxProblem& p) {
     with_tile<AF>(t, [&](auto X) {
       using T = decltype(X);
       const Cost c = Tiles<AF>::cost[t];
-      // a tile of y stays below 2^31 bytes
-      if (t < 3 && p.n > ((INT64_C(1) << 31) - 1) / 4 / T::BM) return;
-      Plan q{t, 1, (p.m + T::BM - 1) / T::BM, (p.n + T::BN - 1) / T::BN};
-      double rows = (double)q.tiles_m;
-      if (p.offsets) {
-        const int64_t G = p.m < p.experts + 1 ? p.m : p.experts + 1;
-        q.tiles_m = G + (p.m - G) / T::BM;
-        rows = (double)p.m / T::BM + 0.5 * G;  // half a tile lost to each group
-      }
-      for (uint32_t s = 1; s <= (p.offsets ? 1 : kMaxSplits) && 2 * s <= (s == 1 ? 2 : steps); s *= 2) {
+      const double G = (double)most_groups(p);
+      const double rows = p.offsets ? (double)p.m / T::BM + 0.5 * G  // half a tile lost to each group
+                                    : (double)((p.m + T::BM - 1) / T::BM);
+      for (uint32_t s = 1; s <= kMaxSplits; s *= 2) {
+        const Plan q = plan_on<T>(p, t, s);
+        if (q.tile < 0) continue;
         const int64_t n = (int64_t)(rows * (double)q.tiles_n + 0.5) * s;
         const double k = (double)((steps + s - 1) / s), find = p.offsets ? 2.0 : 0.0;  // the walk of the offsets
         const double alone = find + c.first + c.step * k, pair = find + c.first2 + c.step2 * k;
@@ -651,11 +663,9 @@ Plan make_plan(const MxProblem& p) {
         double us = full * (T::PER_CU == 2 ? pair : alone);
         if (rest) us += rest <= cus ? alone : pair;
         if (s > 1) us += 3.0 + (double)s * p.m * p.n * 8 / 4e6;
-        if ((q.tiles_m * q.tiles_n * s + 7) * T::THREADS > kMaxLaunchThreads) continue;
         if (best.tiles_m == 0 || us < least) {
           least = us;
           best = q;
-          best.splits = s;
         }
       }
     });
@@ -693,8 +703,7 @@ hipError_t launch_tile(const MxProblem& p, const GemmArgs& g, uint32_t blocks, h
 }
 
 template <int AF>
-hipError_t launch_gemm_format(const MxProblem& p, hipStream_t stream) {
-  const Plan q = make_plan<AF>(p);
+hipError_t launch_gemm_format(const MxProblem& p, const Plan& q, hipStream_t stream) {
   GemmArgs g{(uint32_t)q.tiles_m, (uint32_t)q.tiles_n, q.splits, nullptr};
   if (q.splits > 1) {
     char* ws = nullptr;
@@ -723,8 +732,39 @@ int64_t mx_linear_blocks(int x_fmt, const MxProblem& p) {
 }
 
 hipError_t launch_mx_linear(int x_fmt, const MxProblem& p, hipStream_t stream) {
-  if (skinny(p)) return launch_mx_skinny(x_fmt, p, stream);
-  return x_fmt == kMxFp8 ? launch_gemm_format<kMxFp8>(p, stream) : launch_gemm_format<kMxFp4>(p, stream);
+  if (skinny(p)) return launch_mx_skinny(x_fmt, p, mx_skinny_shape(x_fmt, p), stream);
+  return x_fmt == kMxFp8 ? launch_gemm_format<kMxFp8>(p, make_plan<kMxFp8>(p), stream)
+                         : launch_gemm_format<kMxFp4>(p, make_plan<kMxFp4>(p), stream);
+}
+
+extern "C" int32_t w4_mx_kernel_of(int32_t x_fmt, int32_t experts, int64_t n, int64_t k, int64_t m) {
+  static const int32_t some = 0;
+  const MxProblem p{nullptr, nullptr, nullptr, nullptr, experts ? &some : nullptr, nullptr, nullptr, m, n, k, m,
+                    experts ? experts : 1, 0};
+  if (skinny(p)) return 256 + mx_skinny_shape(x_fmt, p);
+  const Plan q = x_fmt == kMxFp8 ? make_plan<kMxFp8>(p) : make_plan<kMxFp4>(p);
+  return 16 * (int32_t)q.splits + q.tile;
+}
+
+extern "C" int32_t w4_mx_product_on(int32_t kernel, int32_t x_fmt, int32_t experts, int64_t n, int64_t k,
+                                    const uint8_t* w, const uint8_t* w_scales, int64_t tokens, const uint8_t* x,
+                                    const uint8_t* x_scales, int64_t rows, const int32_t* offsets,
+                                    const int32_t* row_index, void* y, int32_t y_bf16, void* stream) {
+  const MxProblem p{w, w_scales, x, x_scales, offsets, row_index, y, rows, n, k, tokens, offsets ? experts : 1, y_bf16};
+  const hipStream_t on = static_cast<hipStream_t>(stream);
+  if (kernel >= 256) {
+    if (kernel > 258 || (!offsets && rows > 16)) return hipErrorInvalidValue;
+    return launch_mx_skinny(x_fmt, p, kernel - 256, on);
+  }
+  const uint32_t parts = (uint32_t)kernel / 16;
+  if (kernel % 16 > 4 || parts < 1 || parts > kMaxSplits) return hipErrorInvalidValue;
+  auto go = [&](auto AF) -> hipError_t {
+    const Plan q = with_tile<decltype(AF)::value>(kernel % 16, [&](auto X) {
+      return plan_on<decltype(X)>(p, kernel % 16, parts);
+    });
+    return q.tile < 0 ? hipErrorInvalidValue : launch_gemm_format<decltype(AF)::value>(p, q, on);
+  };
+  return x_fmt == kMxFp8 ? go(std::integral_constant<int, kMxFp8>{}) : go(std::integral_constant<int, kMxFp4>{});
 }
 
 }  // namespace w4

@@ -242,10 +242,16 @@ using Long = Shape<2, 1, 4>;
 // tiles) 47.5 / 33.7 / 32.2; 256 rows over 63 experts of 4096 x 1024 85 / 40 / 34.
 // One row of x to four is loaded by one instruction a step instead of four, so
 // the split shape pays up to twice the tiles there.
+constexpr int kSplit = 0, kWide = 1, kLong = 2;
+int shape_by(int64_t tiles, bool few) {
+  if (tiles <= (few ? 2048 : 1024)) return kSplit;
+  return tiles <= 8192 ? kWide : kLong;
+}
+
 template <typename F>
-auto by_shape(int64_t tiles, bool few, F&& f) {
-  if (tiles <= (few ? 2048 : 1024)) return f(Split{});
-  return tiles <= 8192 ? f(Wide{}) : f(Long{});
+auto with_shape(int shape, F&& f) {
+  if (shape == kSplit) return f(Split{});
+  return shape == kWide ? f(Wide{}) : f(Long{});
 }
 
 // Tiles of up to 16 rows of y that the groups can make at most: with G groups
@@ -262,17 +268,21 @@ bool few_rows(int x_fmt, const MxProblem& p) { return p.m <= (x_fmt == kMxFp8 ? 
 
 }  // namespace
 
+int mx_skinny_shape(int x_fmt, const MxProblem& p) {
+  return shape_by(row_tiles(p) * ((p.n + 15) / 16), few_rows(x_fmt, p));
+}
+
 int64_t mx_skinny_blocks(int x_fmt, const MxProblem& p) {
-  return by_shape(row_tiles(p) * ((p.n + 15) / 16), few_rows(x_fmt, p), [&](auto S) {
+  return with_shape(mx_skinny_shape(x_fmt, p), [&](auto S) {
     using T = decltype(S);
     const int64_t blocks = row_tiles(p) * ((p.n + T::BN - 1) / T::BN);
     return blocks * (T::KS * T::WN * 64) > kMaxLaunchThreads ? INT64_C(1) << 31 : blocks;
   });
 }
 
-hipError_t launch_mx_skinny(int x_fmt, const MxProblem& p, hipStream_t stream) {
+hipError_t launch_mx_skinny(int x_fmt, const MxProblem& p, int shape, hipStream_t stream) {
   const bool few = few_rows(x_fmt, p), dword = p.k % 128 == 0;
-  return by_shape(row_tiles(p) * ((p.n + 15) / 16), few, [&](auto S) {
+  return with_shape(shape, [&](auto S) {
     using T = decltype(S);
     const uint32_t tiles_n = (uint32_t)((p.n + T::BN - 1) / T::BN);
     const dim3 grid(tiles_n * (uint32_t)row_tiles(p)), block(T::KS * T::WN * 64);
