@@ -22,9 +22,10 @@
  * --------------------------------
  *  - Pointers are DEVICE pointers owned by the caller, all on the current
  *    device (hipSetDevice), as is `stream`; the library keeps none of them
- *    after returning.  It allocates no memory, except w4_gemm and
- *    w4_gemv with m >= 2, which keep a device workspace per (device, stream;
- *    hipStreamPerThread: per thread) for the process's life (see there).
+ *    after returning.  It allocates no memory, except w4_gemm, w4_gemv with
+ *    m >= 2 and w4_mx_linear with m > 16, which keep a device workspace per
+ *    (device, stream; hipStreamPerThread: per thread) for the process's life
+ *    (see there).
  *  - `stream` is a hipStream_t (NULL = the null stream).  A call only enqueues
  *    work on it; it never synchronises the stream or the device.
  *  - All validation happens on the host before anything is enqueued.  On any
@@ -488,11 +489,13 @@ w4_status w4_mx_dequant(int32_t format, int64_t rows, int64_t k, const uint8_t* 
  *       (residual == NULL: h = x, residual_out is not used);
  *   v = h * gamma / sqrt(sum_c h^2 / k + eps): the sum and the row's factor
  *       in fp64, v within 4 * 2^-24 of it in fp32 for every finite h whose v
- *       is a normal fp32 number;
+ *       and v / gamma are normal fp32 numbers;
  *   y = RNE_T(v) unless y is NULL; elements, scales = w4_mx_quantize(v) unless
  *       elements is NULL.  One of the two must be given.
- * The sums are the same bits for the same shape.  A NaN or an infinity in a row
- * of h makes the row's v NaN as IEEE arithmetic does, and so its blocks.
+ * The sums are the same bits for the same shape.  A NaN in a row of h makes all
+ * of the row's v NaN, and so its blocks, as does a row of zeros with eps = 0.  An
+ * infinity makes the row's factor 0: v is 0, and NaN where h is infinite, which
+ * takes those values' blocks only.
  * residual_out may be the same buffer as residual or x; y likewise as x or
  * residual when residual_out is another one.
  * x, residual, residual_out, y [rows][k]; gamma [k].  All 16-byte aligned.
@@ -516,7 +519,7 @@ w4_status w4_mx_rmsnorm(int32_t format, int64_t rows, int64_t k, const void* x,
  * that takes 8-bit elements at all.  It costs 4e-6 of the result in the 2-norm
  * on normal data, at most 7 * 2^-13 = 8.6e-4 of sum_c |X W| (one product in eight
  * 2^13 times the others).  Both stay within the GEMV tolerance, 1e-3 * sum_c
- * |X W| + 1e-6, up to k = 157,000 (MXFP8) and 1,000,000 (MXFP4), above which the
+ * |X W| + 1e-6, up to k = 153,000 (MXFP8) and 1,000,000 (MXFP4), above which the
  * fp32 sums' bound alone passes what is left of it (bf16
  * y: plus 2^-8 |y|).  k == 0 (with m, n > 0): y = +0.  NaN blocks and elements
  * make their row's (column's) results NaN.
