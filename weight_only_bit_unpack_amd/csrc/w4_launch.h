@@ -113,7 +113,7 @@ hipError_t launch_mx_dequant(int fmt, int64_t rows, int64_t k, const uint8_t* q,
 hipError_t launch_mx_rmsnorm(int fmt, int64_t rows, int64_t k, const void* x, const void* residual,
                              const void* gamma, int dtype, float eps, void* residual_out, void* y,
                              uint8_t* q, uint8_t* scales, hipStream_t stream);
-// blocks of the product's launch; 2^31 or more: too many for a launch
+// blocks of the product's launch at most; 2^31 or more: too many for a launch
 int64_t mx_linear_blocks(int x_fmt, const MxProblem& p);
 hipError_t launch_mx_linear(int x_fmt, const MxProblem& p, hipStream_t stream);
 // For the tests, which name the kernel that they run: kernel 16 * parts of k +

@@ -728,6 +728,12 @@ hipError_t launch_gemm_format(const MxProblem& p, const Plan& q, hipStream_t str
 
 int64_t mx_linear_blocks(int x_fmt, const MxProblem& p) {
   if (skinny(p)) return mx_skinny_blocks(x_fmt, p);
+  // No tile is smaller than 64 x 128 (nor has more threads) and k has at most
+  // kMaxSplits parts: where a launch holds the blocks of that, it holds any
+  // plan's, and the costs are computed by the launch only.
+  const int64_t groups = p.offsets ? most_groups(p) : 1;
+  const int64_t most = (groups + p.m / 64) * ((p.n + 127) / 128) * (p.offsets ? 1 : kMaxSplits);
+  if ((most + 7) * 512 <= kMaxLaunchThreads) return most;
   return (x_fmt == kMxFp8 ? make_plan<kMxFp8>(p) : make_plan<kMxFp4>(p)).blocks();
 }
 
