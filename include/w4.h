@@ -76,7 +76,9 @@ typedef enum {
   W4_OK = 0,
   W4_EINVAL = 1,       /* NULL pointer for a non-empty buffer, bad enum, negative size */
   W4_ESHAPE = 2,       /* k not a multiple of the call's group, m outside the call's
-                          range, or a size above the call's stated limit               */
+                          range, or a size above the call's stated limit: in the matrix
+                          calls also 2^32 threads of work (a GEMV of 2^30 rows of the
+                          weight, a GEMM with 2^35 values of x or 2^38 of Y)            */
   W4_EALIGN = 3,       /* a pointer not aligned as the call states                      */
   W4_EUNSUPPORTED = 4, /* a codec / dtype combination the call does not provide         */
   W4_EHIP = 5          /* the kernel launch failed (hipGetLastError)                    */
@@ -393,7 +395,7 @@ w4_status w4_linear(int32_t codec, int64_t n, int64_t k, const uint8_t* packed,
  *    kernel trusts the device copy: it must equal an array the plan accepted.
  * Errors: W4_EINVAL / W4_ESHAPE / W4_EALIGN / W4_EUNSUPPORTED as for w4_gemv
  * (the plan reports the first failing problem's status and writes nothing to
- * *info); W4_ESHAPE when the problems need more than 2^31 - 1 tiles;
+ * *info); W4_ESHAPE when the problems need 2^24 tiles or more;
  * w4_gemv_batched returns W4_EINVAL when m differs from info->m or
  * info->tile_rows is not one the plan can choose.
  */

@@ -68,7 +68,9 @@ w4_status check_matmul(int32_t codec, int64_t n, int64_t k, const uint8_t* packe
   return W4_OK;
 }
 
-w4_status launched(hipError_t e) { return e == hipSuccess ? W4_OK : W4_EHIP; }
+w4_status launched(hipError_t e) {
+  return e == hipSuccess ? W4_OK : e == w4::kTooLarge ? W4_ESHAPE : W4_EHIP;
+}
 
 w4::GemvProblem problem(int64_t n, int64_t k, const uint8_t* packed, const uint16_t* scales,
                         const uint16_t* codebook, const uint16_t* x, void* y) {
@@ -289,7 +291,7 @@ w4_status w4_gemv_batched_plan(int32_t codec, int32_t m, int32_t y_dtype,
     while (rows > 16 && tiles_of(rows) < w4::kGemvBatchedMinTiles) rows /= 2;
   }
   total = tiles_of(rows);
-  if (total > 0x7FFFFFFF) return W4_ESHAPE;
+  if (w4::too_large(total, 256)) return W4_ESHAPE;
   // Work is handed out in tile order; giving the longest rows (largest k) the
   // first tiles leaves short tiles for the end of the launch.
   std::vector<int32_t> order((size_t)count);
@@ -331,7 +333,7 @@ w4_status w4_gemv_batched(int32_t codec, int32_t m, int32_t y_dtype,
     return W4_EINVAL;
   if (!problems_device) return W4_EINVAL;
   if (!aligned(problems_device, 16)) return W4_EALIGN;
-  if (info->total_tiles > 0x7FFFFFFF) return W4_ESHAPE;
+  if (w4::too_large(info->total_tiles, 256)) return W4_ESHAPE;
   return launched(w4::launch_gemv_batched(
       codec, reinterpret_cast<const w4::GemvProblem*>(problems_device), info->count,
       info->total_tiles, info->k_max, info->tile_rows, m, y_dtype == W4_BF16,

@@ -618,6 +618,7 @@ struct GemmPlan {
   int S;
   uint32_t tiles_m, tiles_n, tiles;
   size_t xpk_bytes, per_split, bytes;
+  int64_t pack_blocks;  // of pack_activations
   GemmPlan(int64_t n, int64_t k, int m, int cus) {
     S = gemm_splits(n, k, m, cus, BMT, Tile<BMT>::BK);
     tiles_n = (uint32_t)((n + BN - 1) / BN);
@@ -625,6 +626,7 @@ struct GemmPlan {
     tiles = tiles_n * tiles_m;
     xpk_bytes = (size_t)tiles_m * BMT * k * 2;
     per_split = (size_t)tiles * BMT * BN;  // floats
+    pack_blocks = (int64_t)tiles_m * (BMT / 32) * (k / 64);
     bytes = xpk_bytes + (S > 1 ? (size_t)S * per_split * sizeof(float) : 0);
   }
 };
@@ -637,6 +639,7 @@ hipError_t launch_gemm_shape(int codec, const GemvProblem& p, int m, int y_bf16,
   const GemmPlan<BMT> g(p.n, p.k, m, device_cus());
   const int S = g.S;
   const uint32_t tiles_m = g.tiles_m, tiles = g.tiles;
+  if (too_large(g.pack_blocks, 256) || too_large((int64_t)g.tiles_m * g.tiles_n * S, 512)) return kTooLarge;
   const size_t xpk_bytes = g.xpk_bytes, per_split = g.per_split;
   hipError_t e = hipSuccess;
   if (!ws) {
@@ -645,7 +648,7 @@ hipError_t launch_gemm_shape(int codec, const GemvProblem& p, int m, int y_bf16,
   }
   u32x4* xpk = reinterpret_cast<u32x4*>(ws);
   float* partial = S > 1 ? reinterpret_cast<float*>(ws + xpk_bytes) : nullptr;
-  pack_activations<<<dim3((uint32_t)(tiles_m * (BMT / 32) * (p.k / 64))), dim3(256), 0, stream>>>(
+  pack_activations<<<dim3((uint32_t)g.pack_blocks), dim3(256), 0, stream>>>(
       reinterpret_cast<const u32x4*>(p.x), xpk, m, p.k);
   e = hipGetLastError();
   if (e != hipSuccess) return e;

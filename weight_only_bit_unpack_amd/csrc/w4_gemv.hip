@@ -742,6 +742,7 @@ hipError_t launch_one(const GemvProblem& p, int m, int y_bf16, const GemvShape& 
   constexpr int WAVES = KSPLIT > 4 ? KSPLIT : 4;
   const int rows = 16 * (WAVES / KSPLIT);
   const int64_t blocks = (p.n + rows - 1) / rows;
+  if (too_large(blocks, 64 * WAVES)) return kTooLarge;
   Slicing sl{sh.kslices, sh.slice_steps, nullptr};
   if (sh.kslices > 1) {
     char* ws = nullptr;

@@ -10,6 +10,9 @@ namespace w4 {
 
 // A launch holds fewer than 2^32 threads (HIP cuts a larger one without an error).
 constexpr int64_t kMaxLaunchThreads = 0xFFFFFFFF;
+// What a launcher returns, before it enqueues anything, for a size that needs more.
+constexpr hipError_t kTooLarge = hipErrorInvalidConfiguration;
+inline bool too_large(int64_t blocks, int threads) { return blocks > kMaxLaunchThreads / threads; }
 
 // f(first, count) over parts of at most `most` of `total`, until one fails: the
 // launches of an elementwise call.
