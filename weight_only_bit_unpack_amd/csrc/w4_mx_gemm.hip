@@ -5,18 +5,23 @@
 // v_mfma_scale_f32_32x32x64_f8f6f4 takes the stored elements and scale bytes as
 // they are: nothing is rebuilt, and the sums are the matrix core's fp32.
 //
-// Bound by how far a step's matrix instructions and LDS accesses overlap: a step
-// of 256 x 256 x 256 (MXFP4) is 2048 cycles of matrix instructions on each SIMD
-// and 256 KB through the LDS, and takes 2.0 us, about 4100 cycles at the 1.9 to
-// 2.1 GHz that the card's power leaves under this load; in smaller tiles, by a
-// step's latencies, barrier to barrier.  The copies are no bound: global to LDS
-// reaches 64 bytes a cycle and CU from L2, the steps need 20 to 30.
+// Bound by the waves' waits for each other: a step of 256 x 256 x 256 (MXFP4) is
+// 2048 cycles of matrix instructions on each SIMD and takes 2.0 us, about 4100
+// cycles at the 1.9 to 2.1 GHz that the card's power leaves under this load.
+// Counters of 4096 x 11008 x 4096: matrix cores busy 42% of the cycles, LDS 20%,
+// and the eight waves of a CU, which meet at one barrier a step, 27% of their time
+// in waits (1.4% for the LDS to take an instruction).  In the 64 x 128 tiles a
+// wave has one 32 x 32 accumulator, and a step's LDS reads, three KB a matrix
+// instruction, hold it too.  The copies are no bound: global to LDS reaches 64
+// bytes a cycle and CU from L2, the steps need 20 to 30.
 //
-// Measured (HIP graph replays, operands larger than the L2): 4096 x 11008 x
-// 4096, MXFP4 to fp32, 125 us (3.0 PFLOP/s); 256 x 8192 x 8192, MXFP8 to bf16,
-// 23 us (1.5); 8192 rows over 32 experts of 4096 x 2048, MXFP8, 106 to 113 us by
-// machine (1.2 to 1.3);
-// 3001 rows over 7 experts of 2048 x 5632, MXFP4, 32 us (2.1).  Short k is held
+// Measured (HIP graph replays, three sets of operands in turn, by machine): 4096
+// x 11008 x 4096, MXFP4 to fp32, 124 to 127 us (2.9 to 3.0 PFLOP/s), MXFP8 to
+// bf16 181 us (2.0); 256 x 8192 x 8192, MXFP8 to bf16, 22 to 23 us (1.5); 8192
+// rows over 32 experts of 4096 x 2048, MXFP8, 106 to 113 us (1.2 to 1.3); 3001
+// rows over 7 experts of 2048 x 5632, MXFP4, 32 to 35 us (2.0 to 2.1).  A k that is
+// no multiple of 128 has no steps without conditions: 4096 x 2880 x 2880, MXFP8,
+// 59 us (1.1), at 2816 46 us (1.4).  Short k is held
 // by a tile's 4 to 8 us of start and end (the walk of the offsets, the first
 // copies, the stores, the next block's launch).
 //
@@ -637,10 +642,11 @@ Plan plan_on(const MxProblem& p, int t, uint32_t s) {
 
 // The tile and, for one weight, the parts of k that the costs above say take
 // the least time; the parts' sums cost a launch (3 us) and their bytes, written
-// and read, at 4 TB/s.  Examples (us, measured, the five tiles, each
-// with its least parts): 256 x 8192 x 8192, MXFP8, 32 / 29 / 29 / 24 / 26, the
-// fourth is taken; 4096 x 11008 x 4096, MXFP4, 125 / 153 / 190 / 211 / 200; 3001
-// rows over 7 experts of 2048 x 5632, MXFP4, 45 / 33 / 41 / 42 / 42.
+// and read, at 4 TB/s.  Examples (us, graph replays, the five tiles, each
+// with its best of 1, 2 and 4 parts): 256 x 8192 x 8192, MXFP8, 34 / 30 / 30 / 22 /
+// 25, the fourth is taken; 4096 x 11008 x 4096, MXFP4, 127 / 152 / 185 / 210 / 202;
+// 3001 rows over 7 experts of 2048 x 5632, MXFP4, 46 / 34 / 43 / 44 / 44; 8192 rows
+// over 32 experts of 4096 x 2048, MXFP8, 113 / 141 / 126 / 168 / 130.
 template <int AF>
 Plan make_plan(const MxProblem& p) {
   const int64_t steps = (p.k + 255) / 256, cus = device_cus();

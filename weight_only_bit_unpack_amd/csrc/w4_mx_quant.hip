@@ -5,11 +5,11 @@
 // quad of lanes one block of 32, so the block's maximum is two DPP steps and
 // every load and store instruction covers contiguous memory.
 //
-// Measured (kernel trace; a 1 GiB copy on the same card moves 5.2 TB/s):
-// quantize of 11008 x 4096 bf16 to MXFP4 17.8 us (114 MB, 6.4 TB/s, part of it
-// from the 256 MB cache), the rebuild to bf16 17.6 us; MXFP8 8192 x 4096 rebuilt
-// 16.2 us (102 MB, 6.3 TB/s); the norm with its residual, 8192 x 4096 bf16 to
-// MXFP8, 47.6 us (236 MB, 5.0 TB/s), one row of 2048 2.4 us.
+// Measured (kernel trace over three inputs in turn; a 1 GiB copy on such a card
+// moves 5.2 TB/s): quantize of 11008 x 4096 bf16 to MXFP4 20.6 us (114 MB, 5.5
+// TB/s), the rebuild to bf16 17.7 us; MXFP8 8192 x 4096 rebuilt 16.0 us (102 MB,
+// 6.3 TB/s, part of it from the 256 MB cache); the norm with its residual, 8192 x
+// 4096 bf16 to MXFP8, 49.9 us (236 MB, 4.7 TB/s), one row of 2048 2.8 us.
 #include <type_traits>
 
 #include "w4_launch.h"

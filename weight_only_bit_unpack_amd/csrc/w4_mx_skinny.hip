@@ -11,10 +11,11 @@
 // share the 16 R rows, wave i takes the steps i, i + KS, ..., and their sums
 // are added in wave order through LDS.
 //
-// Measured (HIP graph replays, weights larger than the caches in turn): one
-// token, 4096 -> 11008, 6.8 us (3.5 TB/s, launch included; an empty product
-// takes about 2.9); 13 rows of 4095 x 5632, fp4, 5.2 us; 96 rows over 29
-// experts of 4096 x 2048 32 us (4.0 TB/s).
+// Measured (HIP graph replays, three weights in turn; calls in a row overlap
+// their starts and ends and take 6.2, 4.9 and 31): one token, 4096 -> 11008, 6.8
+// us (3.5 TB/s with the start and end, 1.4 us in a kernel that does nothing); 13
+// rows of 4095 x 5632, fp4, 5.2 us; 96 rows over 29 experts of 4096 x 2048 32 us
+// (4.0 TB/s).
 #include "w4_launch.h"
 #include "w4_mx_device.h"
 #include "w4_mx_group.h"
