@@ -250,3 +250,23 @@ def test_kernels_that_do_not_fit_are_refused(w4):
             run(w4, kernel, "fp8", x, weight, y, o)
     torch.cuda.synchronize()
     assert bool((y == 0).all())
+
+
+@pytest.mark.parametrize("fmt,kernel", ALL)
+def test_outputs_on_element_boundaries(w4, fmt, kernel):
+    """y needs its element's alignment only: one element past a wider boundary, with
+    even and odd widths."""
+    g = torch.Generator("cuda").manual_seed(kernel)
+    bm, bn = (16, 64) if kernel >= 256 else TILE[fmt][kernel % 16]
+    for n in (bn + 30, bn + 13):
+        m, k = (13 if kernel >= 256 else bm + 5), 1056
+        report("mx_unaligned_y", fmt=fmt, kernel=kernel, n=n)
+        x, w = operand(g, (m,), k, fmt, 3), operand(g, (n,), k, "fp4", 2)
+        want = exact(x[2], w[2])
+        for dtype in (F32, BF16):
+            for off in (1, 2, 3):
+                buf = torch.full((m * n + 8,), 7.0, dtype=dtype, device="cuda")
+                y = buf[off:off + m * n].view(m, n)
+                run(w4, kernel, fmt, x, w, y)
+                assert equal(y, want)
+                assert bool((buf[:off] == 7.0).all()) and bool((buf[off + m * n:] == 7.0).all())
