@@ -23,9 +23,9 @@
  *  - Pointers are DEVICE pointers owned by the caller, all on the current
  *    device (hipSetDevice), as is `stream`; the library keeps none of them
  *    after returning.  It allocates no memory, except w4_gemm, w4_gemv with
- *    m >= 2 and w4_mx_linear with m > 16, which keep a device workspace per
- *    (device, stream; hipStreamPerThread: per thread) for the process's life
- *    (see there).
+ *    m >= 2, w4_mx_linear with m > 16 and the calls on bf16 activations and
+ *    MXFP4 weights, which keep a device workspace per (device, stream;
+ *    hipStreamPerThread: per thread) for the process's life (see there).
  *  - `stream` is a hipStream_t (NULL = the null stream).  A call only enqueues
  *    work on it; it never synchronises the stream or the device.
  *  - All validation happens on the host before anything is enqueued.  On any
@@ -561,6 +561,80 @@ w4_status w4_mx_grouped_linear(int32_t x_format, int32_t experts, int64_t n, int
                                const uint8_t* x, const uint8_t* x_scales, int64_t rows,
                                const int32_t* offsets, const int32_t* row_index, void* y,
                                int32_t y_dtype, void* stream);
+
+/*
+ * ---- 16-bit activations on MXFP4 weights ----------------------------------
+ * The products of an MXFP4 weight with activations that stay in bf16, forward
+ * and backward, for serving without quantized activations and for training
+ * around frozen 4-bit weights.  W_hat, the weight's values, are those that
+ * w4_mx_dequant gives as bf16 (NaN in a block of scale 255).
+ *
+ * Conventions of the four calls: sums are fp32, in the matrix core; bf16
+ * products are exact in fp32, so an fp32 output is within (terms / 16 + 40) *
+ * 2^-24 of the sum of the products' magnitudes, and a bf16 output (RNE) within
+ * 2^-9 |y| more.  The same inputs give the same bits, also with other rows
+ * beside them as long as m stays the same.  A NaN or an infinity in a row of x (or
+ * of dy) reaches that row's outputs only, one in a weight its row's (backward:
+ * its columns') only.  k % 32 == 0; any other size, m included, may be 0: an empty
+ * sum is +0, an empty output nothing to do.
+ * x, dy, dh, gu (where read), dgu and w, w_scales 16-byte aligned; y and dx 4-byte
+ * (fp32) or 2-byte (bf16) aligned, as is gu where it is written.
+ * Errors: W4_EINVAL (bad activation, negative size, null pointer), W4_ESHAPE
+ * (k % 32 != 0, k above W4_MAX_MATMUL_K, more than W4_MAX_MX_N rows of the weight,
+ * m above 2^31 - 1, more tiles than 2^32 threads work on), W4_EALIGN,
+ * W4_EUNSUPPORTED (output dtype), W4_EHIP.
+ * Workspace: a product with few output tiles may split its sum into S <= 8 parts
+ * and enqueue a second kernel that adds them in order, S * 4 bytes per sum; a
+ * backward product whose summed length (n; gated 2 n) is not a multiple of 8
+ * first copies its rows, 2 bytes a value, padded to one.  Both are kept per
+ * (device, stream) exactly as for w4_gemm (see there, also for capture into a
+ * graph).
+ */
+typedef enum {
+  W4_SILU = 0,     /* g / (1 + e^-g) */
+  W4_GELU = 1,     /* g Phi(g), Phi the normal distribution's */
+  W4_GELU_TANH = 2 /* g (1 + tanh(sqrt(2/pi) (g + 0.044715 g^3))) / 2 */
+} w4_activation;
+
+/*
+ * w4_mx_linear_bf16 -- y[i][r] = sum_c x[i][c] W_hat[r][c]: W MXFP4 [n][k], x bf16
+ * [m][k], y [m][n] of y_dtype W4_F32 or W4_BF16.
+ */
+w4_status w4_mx_linear_bf16(int64_t n, int64_t k, const uint8_t* w, const uint8_t* w_scales,
+                            const uint16_t* x, int64_t m, void* y, int32_t y_dtype, void* stream);
+
+/*
+ * w4_mx_gated_linear -- a gated feed-forward block up to its second product, in one
+ * kernel: W [2 n][k] holds n gate rows, then n up rows;
+ *   g = x W_gate^T, u = x W_up^T;  y = act(g) * u  [m][n]
+ * from the fp32 sums, rounded once.  gu (or NULL): bf16 [m][2 n], g and u rounded,
+ * for w4_mx_gated_linear_grad.
+ */
+w4_status w4_mx_gated_linear(int32_t act, int64_t n, int64_t k, const uint8_t* w,
+                             const uint8_t* w_scales, const uint16_t* x, int64_t m, uint16_t* gu,
+                             void* y, int32_t y_dtype, void* stream);
+
+/*
+ * w4_mx_linear_grad -- the gradient of w4_mx_linear_bf16's input (the weights are
+ * frozen): dx[i][c] = sum_r dy[i][r] W_hat[r][c], dy bf16 [m][n], dx [m][k] of
+ * dx_dtype W4_F32 or W4_BF16.
+ */
+w4_status w4_mx_linear_grad(int64_t n, int64_t k, const uint8_t* w, const uint8_t* w_scales,
+                            const uint16_t* dy, int64_t m, void* dx, int32_t dx_dtype,
+                            void* stream);
+
+/*
+ * w4_mx_gated_linear_grad -- backward of w4_mx_gated_linear: from dh bf16 [m][n], the
+ * gradient of y, and the gu that the forward call wrote,
+ *   dgu = [dh u act'(g), dh act(g)]  bf16 [m][2 n], computed in fp32 and rounded once
+ *         (the gradients of g and u, which adapters beside the weights need);
+ *   dx = dgu W_hat  [m][k] of dx_dtype, of dgu as it is stored.
+ * dgu may be the same buffer as gu.
+ */
+w4_status w4_mx_gated_linear_grad(int32_t act, int64_t n, int64_t k, const uint8_t* w,
+                                  const uint8_t* w_scales, const uint16_t* dh, const uint16_t* gu,
+                                  int64_t m, uint16_t* dgu, void* dx, int32_t dx_dtype,
+                                  void* stream);
 
 #ifdef __cplusplus
 }

@@ -8,8 +8,12 @@ lists of levels, in fp64: a block's scale exponent is that of its largest
 magnitude less the largest element's, and a value takes the nearest level of
 the scaled grid, the even code on a tie, the largest level beyond the grid.
 
-Pinned against exact rational arithmetic in ``tests/test_oracle_mx.py``.
+Pinned against exact rational arithmetic in ``tests/test_oracle_mx.py``; the
+activations of the gated block against their definitions and differences in
+``tests/test_oracle_mx_gated.py``.
 """
+
+import math
 
 import numpy as np
 
@@ -121,3 +125,43 @@ def grouped_linear(x, w, offsets, row_index=None, rows=None):
             y[lo:hi], b[lo:hi] = linear(xs[lo:hi], w[e])
             y[lo:hi][~ok[lo:hi]] = 0.0
     return y, b
+
+
+# ------------------------------------------------------------------ the gated block
+def _erfc(x):
+    return np.vectorize(math.erfc, otypes=[np.float64])(x)
+
+
+def _sigmoid(z):
+    """1 / (1 + e^-z) without overflow, for either sign."""
+    e = np.exp(-np.abs(z))
+    return np.where(z >= 0, 1.0, e) / (1.0 + e)
+
+
+TANH_A = math.sqrt(2.0 / math.pi)
+
+
+def activation(g, act):
+    """fp64 (act(g), act'(g)) of silu, gelu and gelu_tanh."""
+    g = np.asarray(g, dtype=np.float64)
+    if act == "silu":
+        return g * _sigmoid(g), _sigmoid(g) * (1 + g * _sigmoid(-g))
+    if act == "gelu":
+        phi = 0.5 * _erfc(-g / math.sqrt(2.0))
+        return g * phi, phi + g * np.exp(-0.5 * g * g) / math.sqrt(2.0 * math.pi)
+    if act != "gelu_tanh":
+        raise ValueError(act)
+    z = 2 * TANH_A * (g + 0.044715 * g ** 3)          # (1 + tanh(z / 2)) / 2 = sigmoid(z)
+    slope = 2 * TANH_A * (1 + 3 * 0.044715 * g * g)
+    return g * _sigmoid(z), _sigmoid(z) * (1 + g * _sigmoid(-z) * slope)
+
+
+def gated(g, u, act):
+    """fp64 act(g) * u."""
+    return activation(g, act)[0] * np.asarray(u, dtype=np.float64)
+
+
+def gated_grad(dh, g, u, act):
+    """fp64 gradients of g and u, given that of act(g) * u."""
+    a, d = activation(g, act)
+    return np.asarray(dh) * np.asarray(u) * d, np.asarray(dh) * a

@@ -24,6 +24,7 @@ W4_F32, W4_BF16, W4_F16 = 0, 1, 2
 GROUP = {W4_DYADIC: 64, W4_LUT16: 64, W4_SIGNMAG8: 32, W4_LUT16S: 64, W4_DYADIC5: 64,
          W4_LUT16S_PERM: 64, W4_LUT16S_IL: 64}
 W4_MXFP4, W4_MXFP8 = 0, 1  # MX formats (w4_mx_format)
+W4_SILU, W4_GELU, W4_GELU_TANH = 0, 1, 2  # activations of the gated block (w4_activation)
 IL_RECORD = 144  # bytes of one W4_LUT16S_IL record (256 weights)
 
 if not os.path.exists(LIB_PATH):
@@ -90,6 +91,10 @@ _SIGS = {
     "w4_mx_linear": ([_I32, _I64, _I64, _P, _P, _P, _P, _I64, _P, _I32, _P], _I32),
     "w4_mx_grouped_linear": ([_I32, _I32, _I64, _I64, _P, _P, _I64, _P, _P, _I64, _P, _P, _P, _I32,
                               _P], _I32),
+    "w4_mx_linear_bf16": ([_I64, _I64, _P, _P, _P, _I64, _P, _I32, _P], _I32),
+    "w4_mx_gated_linear": ([_I32, _I64, _I64, _P, _P, _P, _I64, _P, _P, _I32, _P], _I32),
+    "w4_mx_linear_grad": ([_I64, _I64, _P, _P, _P, _I64, _P, _I32, _P], _I32),
+    "w4_mx_gated_linear_grad": ([_I32, _I64, _I64, _P, _P, _P, _P, _I64, _P, _P, _I32, _P], _I32),
 }
 for _name, (_args, _res) in _SIGS.items():
     _fn = getattr(_lib, _name)
@@ -482,3 +487,36 @@ def w4_mx_grouped_linear(xq, xs, wq, ws, offsets, fmt=W4_MXFP8, *, rows=None, y=
     zeros.  Accuracy as w4_mx_linear."""
     return _mx(stream, _w4mx.grouped_linear, xq, xs, wq, ws, offsets, fmt, rows, y,
                _MX_DTYPE.get(y_dtype, -1))
+
+
+# ---- bf16 activations on MXFP4 weights, forward and backward (the weights are frozen)
+def w4_mx_linear_bf16(x, wq, ws, *, y=None, y_dtype=torch.float32, stream=None):
+    """y[m, n] = x[m, k] @ W[n, k]^T with x in bf16 and W (wq, ws) in W4_MXFP4,
+    rebuilt exactly in the kernel; fp32 sums, fp32 or bf16 y, any m (single tokens
+    included)."""
+    return _mx(stream, _w4mx.linear_bf16, x, wq, ws, y, _MX_DTYPE.get(y_dtype, -1))
+
+
+def w4_mx_gated_linear(x, wq, ws, act=W4_SILU, *, gu=None, y=None, y_dtype=torch.float32,
+                       stream=None):
+    """y[m, n] = act(x @ W_gate^T) * (x @ W_up^T) in one kernel: x bf16 [m, k], W
+    (wq [2 n, k/2], ws [2 n, k/32]) in W4_MXFP4 with the gate rows first, act
+    W4_SILU, W4_GELU or W4_GELU_TANH.  ``gu`` (a bf16 tensor [m, 2 n]) also gets
+    both products, which w4_mx_gated_linear_grad needs."""
+    return _mx(stream, _w4mx.gated_linear, x, wq, ws, act, gu, y, _MX_DTYPE.get(y_dtype, -1))
+
+
+def w4_mx_linear_grad(dy, wq, ws, *, dx=None, dx_dtype=torch.bfloat16, stream=None):
+    """The gradient of w4_mx_linear_bf16's x: dx[m, k] = dy[m, n] @ W[n, k], dy
+    bf16; fp32 or bf16 dx."""
+    return _mx(stream, _w4mx.linear_grad, dy, wq, ws, dx, _MX_DTYPE.get(dx_dtype, -1))
+
+
+def w4_mx_gated_linear_grad(dh, gu, wq, ws, act=W4_SILU, *, dgu=None, dx=None,
+                            dx_dtype=torch.bfloat16, stream=None):
+    """Backward of w4_mx_gated_linear from dh (bf16 [m, n], the gradient of its y)
+    and the ``gu`` that it wrote.  Returns (dx [m, k], dgu bf16 [m, 2 n]): dgu, the
+    gradients of both products, may be given as ``gu`` to overwrite it; dx is dgu @
+    W of dgu as it is stored."""
+    return _mx(stream, _w4mx.gated_linear_grad, dh, gu, wq, ws, act, dgu, dx,
+               _MX_DTYPE.get(dx_dtype, -1))

@@ -135,4 +135,37 @@ int64_t mx_skinny_blocks(int x_fmt, const MxProblem& p);
 int mx_skinny_shape(int x_fmt, const MxProblem& p);  // 0 .. 2
 hipError_t launch_mx_skinny(int x_fmt, const MxProblem& p, int shape, hipStream_t stream);
 
+// ---- bf16 rows times MXFP4 weights
+// kMxForward: y[m][n] = x w^T.  kMxGated: w holds n gate and n up rows, y[m][n] =
+// act(x gate^T) * (x up^T).  kMxBackward: y[m][k] = x w, x [m][n].
+constexpr int kMxForward = 0, kMxGated = 1, kMxBackward = 2;
+struct MxBf16Problem {
+  const uint8_t* w;         // fp4 elements [n, gated 2 n][k/2]
+  const uint8_t* w_scales;  // [n, gated 2 n][k/32]
+  const uint16_t* x;        // bf16 rows of x_pitch values, whole 16-byte units
+  void* y;
+  uint16_t* gu;             // gated: bf16 [m][2 n], or nullptr
+  int64_t m, n, k, x_pitch;
+  int32_t y_bf16, act, kind;
+};
+// Backward of the gated block: dgu[m][2 n] from dh [m][n] and gu [m][2 n], bf16.
+struct MxGateGrad {
+  const uint16_t* dh;
+  const uint16_t* gu;
+  uint16_t* dgu;
+  int64_t m, n;
+  int32_t act;
+};
+// false: some launch would need more than 2^32 threads
+bool mx_bf16_fits(const MxBf16Problem& p);
+// (w4_mx_bf16_gemm.hip) with a workspace of at least mx_bf16_workspace_bytes
+size_t mx_bf16_workspace_bytes(const MxBf16Problem& p);
+hipError_t launch_mx_bf16_on(const MxBf16Problem& p, char* ws, hipStream_t stream);
+// (w4_mx_bf16.hip) with the library's workspace of the stream.  Backward, x's
+// pitch may be any n: rows of no whole 16-byte units are padded into the
+// workspace first.
+hipError_t launch_mx_bf16(const MxBf16Problem& p, hipStream_t stream);
+// dgu, then (where p.k > 0) p, kMxBackward over dgu
+hipError_t launch_mx_gated_grad(const MxGateGrad& g, const MxBf16Problem& p, hipStream_t stream);
+
 }  // namespace w4

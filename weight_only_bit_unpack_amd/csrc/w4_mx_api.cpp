@@ -6,28 +6,18 @@
 
 #include "w4.h"
 #include "w4_launch.h"
+#include "w4_mx_checks.h"
 
 namespace {
 
-bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+using w4::aligned;
+using w4::check_y;
+using w4::guarded;
 
 bool valid_format(int32_t f) { return f == W4_MXFP4 || f == W4_MXFP8; }
 bool valid_dtype(int32_t d) { return d == W4_F32 || d == W4_BF16 || d == W4_F16; }
 
 constexpr int64_t kMaxBlocks = 0x7FFFFFFF;
-
-w4_status launched(hipError_t e) { return e == hipSuccess ? W4_OK : W4_EHIP; }
-
-// The launchers may allocate a workspace or grow a table of them; nothing they
-// throw passes the C boundary.
-template <typename F>
-w4_status guarded(F&& f) {
-  try {
-    return launched(f());
-  } catch (...) {
-    return W4_EHIP;
-  }
-}
 
 // an elementwise call over rows * k values, one block per 2048 of them
 w4_status check_array(int32_t format, int64_t rows, int64_t k) {
@@ -48,11 +38,6 @@ w4_status check_operands(const void* w, const void* ws, const void* x, const voi
   if (!w || !ws || !x || !xs) return W4_EINVAL;
   if (!aligned(w, 16) || !aligned(ws, 16) || !aligned(x, 16) || !aligned(xs, 16)) return W4_EALIGN;
   return W4_OK;
-}
-
-w4_status check_y(const void* y, int32_t y_dtype) {
-  if (!y) return W4_EINVAL;
-  return aligned(y, y_dtype == W4_F32 ? 4 : 2) ? W4_OK : W4_EALIGN;
 }
 
 }  // namespace

@@ -13,6 +13,7 @@
 
 #include <stdexcept>
 #include <string>
+#include <utility>
 
 #include "w4.h"
 
@@ -110,16 +111,19 @@ Tensor byte_output(PyObject* o, const char* name, at::IntArrayRef shape, const T
   return t;
 }
 
-// y of a product: given, or allocated as y_dtype (a w4_dtype)
-Tensor product_output(PyObject* o, long y_dtype, int64_t m, int64_t n, const Tensor& like, int dev) {
+// y (or dx) of a product: given, or allocated as y_dtype (a w4_dtype)
+Tensor product_output(PyObject* o, long y_dtype, int64_t m, int64_t n, const Tensor& like, int dev,
+                      const char* name = "y") {
   if (o == Py_None) {
-    if (y_dtype != W4_F32 && y_dtype != W4_BF16) throw Refused("y_dtype must be float32 or bfloat16");
+    if (y_dtype != W4_F32 && y_dtype != W4_BF16)
+      throw Refused(std::string(name) + "_dtype must be float32 or bfloat16");
     return empty({m, n}, y_dtype == W4_F32 ? at::kFloat : at::kBFloat16, like);
   }
-  const Tensor& t = tensor(o, "y", dev);
+  const Tensor& t = tensor(o, name, dev);
   if (t.scalar_type() != at::kFloat && t.scalar_type() != at::kBFloat16)
-    throw Refused(std::string("y has dtype ") + c10::toString(t.scalar_type()) + ", expected float32 or bfloat16");
-  need_shape(t, "y", {m, n});
+    throw Refused(std::string(name) + " has dtype " + c10::toString(t.scalar_type()) +
+                  ", expected float32 or bfloat16");
+  need_shape(t, name, {m, n});
   return t;
 }
 
@@ -337,6 +341,108 @@ PyObject* grouped_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
   });
 }
 
+// ---- bf16 rows on MXFP4 weights
+
+// the weight's rows and k
+std::pair<int64_t, int64_t> weight(PyObject* q, PyObject* s, int dev, const uint8_t*& w, const uint8_t*& ws) {
+  const Tensor& wq = bytes(q, "wq", dev);
+  if (wq.dim() != 2) throw Refused("wq must be [n, k/2]");
+  const int64_t rows = wq.size(0), k = 2 * wq.size(1);
+  const Tensor& scales = bytes(s, "ws", dev);
+  need_shape(scales, "ws", {rows, k / 32});
+  w = u8(wq);
+  ws = u8(scales);
+  return {rows, k};
+}
+
+// bf16 [m, n]; m < 0: any number of rows
+const Tensor& bf16_rows(PyObject* o, const char* name, int64_t m, int64_t n, int dev) {
+  const Tensor& t = tensor(o, name, dev);
+  need_dtype(t, name, at::kBFloat16);
+  if (m >= 0) {
+    need_shape(t, name, {m, n});
+  } else if (t.dim() != 2 || t.size(1) != n) {
+    throw Refused(std::string(name) + " has shape " + shape_of(t.sizes()) + ", expected [m, " + std::to_string(n) + "]");
+  }
+  return t;
+}
+
+int64_t halves(int64_t rows) {
+  if (rows % 2) throw Refused("wq has " + std::to_string(rows) + " rows, expected as many gate as up rows");
+  return rows / 2;
+}
+
+const uint16_t* u16(const Tensor& t) { return static_cast<const uint16_t*>(t.const_data_ptr()); }
+uint16_t* u16(Tensor& t) { return static_cast<uint16_t*>(t.data_ptr()); }
+
+// (x, wq, ws, y, y_dtype) -> y
+PyObject* linear_bf16(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 5, [&]() -> PyObject* {
+    const int dev = current_device(a[0], "x");
+    const uint8_t *w, *ws;
+    const auto [rows, k] = weight(a[1], a[2], dev, w, ws);
+    const Tensor& x = bf16_rows(a[0], "x", -1, k, dev);
+    const int64_t m = x.size(0);
+    Tensor y = product_output(a[3], PyLong_AsLong(a[4]), m, rows, x, dev);
+    const w4_status st =
+        w4_mx_linear_bf16(rows, k, w, ws, u16(x), m, y.data_ptr(), dtype_code(y.scalar_type()), stream(dev));
+    return st ? status(st) : THPVariable_Wrap(y);
+  });
+}
+
+// (x, wq, ws, act, gu or None, y, y_dtype) -> y
+PyObject* gated_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 7, [&]() -> PyObject* {
+    const int dev = current_device(a[0], "x");
+    const uint8_t *w, *ws;
+    const auto [rows, k] = weight(a[1], a[2], dev, w, ws);
+    const int64_t out = halves(rows);
+    const Tensor& x = bf16_rows(a[0], "x", -1, k, dev);
+    const int64_t m = x.size(0);
+    const long act = PyLong_AsLong(a[3]);
+    Tensor gu;
+    if (a[4] != Py_None) gu = bf16_rows(a[4], "gu", m, rows, dev);
+    Tensor y = product_output(a[5], PyLong_AsLong(a[6]), m, out, x, dev);
+    const w4_status st = w4_mx_gated_linear(act, out, k, w, ws, u16(x), m, gu.defined() ? u16(gu) : nullptr,
+                                            y.data_ptr(), dtype_code(y.scalar_type()), stream(dev));
+    return st ? status(st) : THPVariable_Wrap(y);
+  });
+}
+
+// (dy, wq, ws, dx, dx_dtype) -> dx
+PyObject* linear_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 5, [&]() -> PyObject* {
+    const int dev = current_device(a[0], "dy");
+    const uint8_t *w, *ws;
+    const auto [rows, k] = weight(a[1], a[2], dev, w, ws);
+    const Tensor& dy = bf16_rows(a[0], "dy", -1, rows, dev);
+    const int64_t m = dy.size(0);
+    Tensor dx = product_output(a[3], PyLong_AsLong(a[4]), m, k, dy, dev, "dx");
+    const w4_status st =
+        w4_mx_linear_grad(rows, k, w, ws, u16(dy), m, dx.data_ptr(), dtype_code(dx.scalar_type()), stream(dev));
+    return st ? status(st) : THPVariable_Wrap(dx);
+  });
+}
+
+// (dh, gu, wq, ws, act, dgu, dx, dx_dtype) -> (dx, dgu)
+PyObject* gated_linear_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
+  return guarded(n, 8, [&]() -> PyObject* {
+    const int dev = current_device(a[0], "dh");
+    const uint8_t *w, *ws;
+    const auto [rows, k] = weight(a[2], a[3], dev, w, ws);
+    const int64_t out = halves(rows);
+    const Tensor& dh = bf16_rows(a[0], "dh", -1, out, dev);
+    const int64_t m = dh.size(0);
+    const Tensor& gu = bf16_rows(a[1], "gu", m, rows, dev);
+    const long act = PyLong_AsLong(a[4]);
+    Tensor dgu = a[5] == Py_None ? empty({m, rows}, at::kBFloat16, dh) : bf16_rows(a[5], "dgu", m, rows, dev);
+    Tensor dx = product_output(a[6], PyLong_AsLong(a[7]), m, k, dh, dev, "dx");
+    const w4_status st = w4_mx_gated_linear_grad(act, out, k, w, ws, u16(dh), u16(gu), m, u16(dgu), dx.data_ptr(),
+                                                 dtype_code(dx.scalar_type()), stream(dev));
+    return st ? status(st) : pair(dx, dgu);
+  });
+}
+
 // (function of a device index that names its current stream)
 PyObject* set_stream_query(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 1, [&]() -> PyObject* {
@@ -348,8 +454,10 @@ PyObject* set_stream_query(PyObject*, PyObject* const* a, Py_ssize_t n) {
 }
 
 #define W4_METHOD(f) {#f, reinterpret_cast<PyCFunction>(reinterpret_cast<void (*)()>(f)), METH_FASTCALL, nullptr}
-PyMethodDef methods[] = {W4_METHOD(quantize), W4_METHOD(dequant),        W4_METHOD(rmsnorm),
-                         W4_METHOD(linear),   W4_METHOD(grouped_linear), W4_METHOD(set_stream_query), {nullptr, nullptr, 0, nullptr}};
+PyMethodDef methods[] = {W4_METHOD(quantize),    W4_METHOD(dequant),           W4_METHOD(rmsnorm),
+                         W4_METHOD(linear),      W4_METHOD(grouped_linear),    W4_METHOD(linear_bf16),
+                         W4_METHOD(gated_linear), W4_METHOD(linear_grad),      W4_METHOD(gated_linear_grad),
+                         W4_METHOD(set_stream_query), {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_w4mx", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 
