@@ -82,6 +82,13 @@ hipError_t launch_gemv_batched(int codec, const GemvProblem* probs_dev, int coun
 // use it), so it never waits for the stream.
 enum { kWorkspaceGemm = 0, kWorkspaceGemv = 1, kWorkspaceMx = 2 };
 hipError_t stream_workspace(int user, hipStream_t stream, size_t bytes, char** out);
+// A number of the calling thread from 1 on, never given again (the system gives
+// an ended thread's id again, while its last kernels may still run).
+uint64_t this_thread();
+// kMxCounters counters of (current device, stream), zeros to begin with: every
+// kernel that counts in them leaves zeros behind (w4_counters.cpp).
+constexpr int kMxCounters = 2048;
+hipError_t stream_counters(hipStream_t stream, uint32_t** out);
 
 // ws: a workspace of at least gemm_workspace_bytes(...) bytes, or nullptr for
 // the library-kept one of the stream (stream_workspace)
@@ -158,9 +165,21 @@ struct MxGateGrad {
 };
 // false: some launch would need more than 2^32 threads
 bool mx_bf16_fits(const MxBf16Problem& p);
-// (w4_mx_bf16_gemm.hip) with a workspace of at least mx_bf16_workspace_bytes
-size_t mx_bf16_workspace_bytes(const MxBf16Problem& p);
-hipError_t launch_mx_bf16_on(const MxBf16Problem& p, char* ws, hipStream_t stream);
+// (w4_mx_bf16_gemm.hip) with the library's workspace of the stream; `reserve` bytes of
+// it (whole 256), before the product's own, are the caller's: fill (or nullptr)
+// enqueues what writes them, and may change the problem
+struct MxBf16Fill {
+  virtual hipError_t operator()(MxBf16Problem& p, char* reserved) = 0;
+};
+hipError_t launch_mx_bf16_with(const MxBf16Problem& p, size_t reserve, MxBf16Fill* fill, hipStream_t stream);
+// For the tests, which name the kernel that they run: 16 * parts of the sum + tile
+// (w4_mx_bf16_gemm.hip), 1024 more where only the last tiles are cut into parts.  The kernel that a product takes:
+extern "C" int32_t w4_mx_bf16_kernel_of(int32_t kind, int64_t n, int64_t k, int64_t m);
+// The product (kind, sizes and pointers as in MxBf16Problem, x without padding)
+// on a kernel of the caller's choice; a hipError_t, an error where it does not fit.
+extern "C" int32_t w4_mx_bf16_product_on(int32_t kernel, int32_t kind, int32_t act, int64_t n, int64_t k,
+                                         const uint8_t* w, const uint8_t* w_scales, const uint16_t* x, int64_t m,
+                                         uint16_t* gu, void* y, int32_t y_bf16, void* stream);
 // (w4_mx_bf16.hip) with the library's workspace of the stream.  Backward, x's
 // pitch may be any n: rows of no whole 16-byte units are padded into the
 // workspace first.

@@ -86,35 +86,27 @@ size_t padded_bytes(int64_t m, int64_t n) {
   return n % 8 ? ((size_t)m * padded_pitch(n) * 2 + 255) / 256 * 256 : 0;
 }
 
-// p with its padded rows at the start of the workspace, and its partial sums
-// behind them; fill(padded, pitch) enqueues what writes the rows
+// The product over rows padded to whole units, which lie in the workspace;
+// write(rows, pitch) enqueues what fills them.
 template <typename F>
-hipError_t launch_padded(MxBf16Problem p, hipStream_t stream, F&& fill) {
-  const size_t rows = padded_bytes(p.m, p.n);
-  p.x_pitch = padded_pitch(p.n);
-  const size_t bytes = rows + mx_bf16_workspace_bytes(p);
-  char* ws = nullptr;
-  hipError_t e = stream_workspace(kWorkspaceMx, stream, bytes, &ws);
-  if (e != hipSuccess) return e;
-  p.x = reinterpret_cast<const uint16_t*>(ws);
-  e = fill(reinterpret_cast<uint16_t*>(ws), p.x_pitch);
-  return e != hipSuccess ? e : launch_mx_bf16_on(p, ws + rows, stream);
-}
-
-hipError_t launch_unpadded(const MxBf16Problem& p, hipStream_t stream) {
-  const size_t bytes = mx_bf16_workspace_bytes(p);
-  char* ws = nullptr;
-  if (bytes) {
-    const hipError_t e = stream_workspace(kWorkspaceMx, stream, bytes, &ws);
-    if (e != hipSuccess) return e;
-  }
-  return launch_mx_bf16_on(p, ws, stream);
+hipError_t launch_padded(const MxBf16Problem& p, hipStream_t stream, F&& write) {
+  struct Fill final : MxBf16Fill {
+    F& write;
+    explicit Fill(F& w) : write(w) {}
+    hipError_t operator()(MxBf16Problem& on, char* ws) override {
+      on.x = reinterpret_cast<const uint16_t*>(ws);
+      return write(reinterpret_cast<uint16_t*>(ws), on.x_pitch);
+    }
+  } fill(write);
+  MxBf16Problem on = p;
+  on.x_pitch = padded_pitch(p.n);
+  return launch_mx_bf16_with(on, padded_bytes(p.m, p.n), &fill, stream);
 }
 
 }  // namespace
 
 hipError_t launch_mx_bf16(const MxBf16Problem& p, hipStream_t stream) {
-  if (p.kind != kMxBackward || p.n % 8 == 0) return launch_unpadded(p, stream);
+  if (p.kind != kMxBackward || p.n % 8 == 0) return launch_mx_bf16_with(p, 0, nullptr, stream);
   return launch_padded(p, stream, [&](uint16_t* rows, int64_t pitch) {
     return in_launches(p.m * pitch, [&](int64_t first, int64_t count, dim3 grid) {
       pad_kernel<<<grid, dim3(256), 0, stream>>>(p.x, p.n, rows, pitch, first, count);
@@ -141,7 +133,7 @@ hipError_t launch_mx_gated_grad(const MxGateGrad& g, const MxBf16Problem& p, hip
   else
     e = any(nullptr, 0);
   if (e != hipSuccess || p.k == 0) return e;
-  return launch_unpadded(p, stream);
+  return launch_mx_bf16_with(p, 0, nullptr, stream);
 }
 
 }  // namespace w4

@@ -18,11 +18,8 @@
 // that a lane ends with both factors.
 //
 // Backward, the sum is over the rows of W, and its 4 bits lie along the other
-// index.  ds_read_b64_tr_b8 gives a lane one byte, two neighbouring columns, of
-// eight rows; each byte is rebuilt with its row's scale, and v_perm pairs rows:
-// tile j takes columns 2 r + j.  The rows' scales, one byte each for 32 columns,
-// are copied a step ahead of the weights and turned by the wave that copied them
-// into 64 bytes a block of columns.
+// index: a step's weights are rebuilt a step ahead, once for the block, to bf16
+// rows in LDS, and ds_read_b64_tr_b16 gives a lane four rows of one column.
 #include <atomic>
 #include <type_traits>
 
@@ -34,41 +31,45 @@
 namespace w4 {
 namespace {
 
-typedef int i32x2 __attribute__((ext_vector_type(2)));
+typedef short i16x4 __attribute__((ext_vector_type(4)));
 
 // A block of BM rows of x by BN columns (forward: weight rows): WM x WN waves,
-// each with MT x 2 accumulators of 32 x 32.  NS steps of 64 in LDS: one read,
-// the others arriving.
-template <int BM_, int BN_, int WM_, int WN_, int NS_>
+// each with MT x 2 accumulators of 32 x 32.  NS (backward: NB) steps of 64 in LDS:
+// one read, the others arriving.
+template <int BM_, int BN_, int WM_, int WN_, int NS_, int NB_>
 struct Tile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_, NB = NB_;
   static constexpr int NW = WM * WN, THREADS = 64 * NW, MT = BM / WM / 32;
   static_assert(BN == 64 * WN && BM == 32 * WM * MT, "waves of 32 MT x 64");
   // 16-byte units of a step: rows of x, weights, scale bytes (a dword each)
   static constexpr int A = BM * 8, W = BN * 2, S = BN / 2;
-  static constexpr int P = BN / 8;  // backward: the scales turned, 64 bytes for 32 columns
+  static constexpr int R = BN * 8;  // backward: 64 rows of BN rebuilt weights
   static constexpr int IA = A / THREADS, IW = W / THREADS, IS = 4 * S / THREADS;  // copies of a wave
   static_assert(IA * THREADS == A && IW * THREADS == W && IS * THREADS == 4 * S, "the waves share the copies");
   static constexpr int COPIES = IA + IW + IS;
-  static constexpr int LDS = NS * (A + W + S) + 2 * P;
-  static_assert(LDS * 16 <= 160 * 1024, "the LDS of a CU");
+  static constexpr int FORWARD = NS * (A + W + S), BACKWARD = NB * (A + W + S) + 2 * R;  // units of LDS
+  static_assert(FORWARD <= 10240 && BACKWARD <= 10240, "the LDS of a CU");
 };
-using T0 = Tile<256, 256, 2, 4, 3>;
-using T1 = Tile<128, 256, 2, 4, 3>;
-using T2 = Tile<128, 128, 2, 2, 3>;
-using T3 = Tile<64, 128, 2, 2, 3>;
-using T4 = Tile<32, 128, 1, 2, 3>;
+using T0 = Tile<256, 256, 2, 4, 3, 2>;
+using T1 = Tile<128, 256, 2, 4, 3, 3>;
+using T2 = Tile<128, 128, 2, 2, 3, 2>;
+using T3 = Tile<64, 128, 2, 2, 3, 3>;
+using T4 = Tile<32, 128, 1, 2, 3, 2>;
 constexpr int kTiles = 5;
 
-constexpr uint32_t kMaxSplits = 8;
+constexpr uint32_t kMaxSplits = 16;
 // An offset past the resource of a tile's outputs (below 2^31 bytes), also with
 // the offset of a row added.
 constexpr uint32_t kStoreOOB = 0x80000000u;
 
+// The first `whole` of the tiles are one block's each.  The sums of the others
+// (all, or what is left of the last round of blocks) are cut into `splits`
+// parts, a block each: a part writes its sums to partial, and the block that
+// counts last adds the parts of its tile in order.  Nobody waits.
 struct GemmArgs {
-  uint32_t tiles_m, tiles_n;
-  uint32_t splits;  // parts of the sum, each to its own fp32 array at partial
-  float* partial;
+  uint32_t tiles_m, tiles_n, whole, splits;
+  uint64_t* partial;  // [tile behind the whole ones][part][BM BN / 2], pairs of fp32
+  uint32_t* counted;  // [tile behind the whole ones], zeros between launches
 };
 
 // What a copy past the end of the summed index reads.
@@ -78,18 +79,21 @@ __device__ const u32x4 kZeros[1] = {};
 // bytes in LDS: the reads of 16 rows take 16 different units of the banks' 256
 // bytes.
 __device__ __forceinline__ int swizzle_x(int row) { return (row >> 1) & 7; }
-// The same for the weights, forward (rows of two units) ...
+// The same for the weights forward (rows of two units).
 __device__ __forceinline__ int swizzle_w(int row) { return (row >> 3) & 1; }
-// ... and backward (rows of U units, read in pairs of units, eight rows at a time).
-template <int U>
-__device__ __forceinline__ int swizzle_wt(int row) {
-  return 2 * (row / (16 / U) % (U / 2));
+// Where unit c of row `row` of the rebuilt weights lies in its row: the writes
+// (16 lanes: rows beside each other, every fourth unit) and the transposing reads
+// (32 lanes: four rows, four units each) both take all of the banks' units.
+template <int BN>
+__device__ __forceinline__ int swizzle_r(int row, int c) {
+  const int n0 = row & 1, n1 = (row >> 1) & 1;
+  return c ^ (n1 << 3 | n0 << 2 | (n0 ^ ((c >> 3) & 1)) << 1 | (BN == 256 ? (c >> 4) & 1 : n1));
 }
 
 template <int KIND, typename T>
 __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem P, GemmArgs G) {
   constexpr bool kBack = KIND == kMxBackward, kGate = KIND == kMxGated;
-  constexpr int MT = T::MT, NS = T::NS;
+  constexpr int MT = T::MT, NS = kBack ? T::NB : T::NS;
   constexpr int U = T::BN / 32;                        // backward: units of a weight row in the tile
   constexpr int OUT = kGate ? T::BN / 2 : T::BN;       // outputs of a row in the tile
   extern __shared__ u32x4 lds[];
@@ -99,13 +103,15 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
   const int r = lane & 31, h = lane >> 5;
 
   // Blocks are dealt to the 8 XCDs round robin; each XCD takes a contiguous
-  // range of the tiles, whose rows of x and w meet in its L2: eight tiles of
-  // rows beside each other, then the next tile of columns.  (The grid is a
-  // multiple of 8.)
-  const uint32_t tiles = G.tiles_m * G.tiles_n, total = tiles * G.splits;
-  const uint32_t range = (total + 7) / 8, L = blockIdx.x % 8 * range + blockIdx.x / 8;
-  if (blockIdx.x / 8 >= range || L >= total) return;
-  const uint32_t split = L / tiles, tile = L % tiles;
+  // range of the whole tiles, and then of the parts, whose rows of x and w meet in
+  // its L2: eight tiles of rows beside each other, then the next tile of columns.
+  // (Each of the two kinds has a multiple of 8 blocks.)
+  const uint32_t first = (G.whole + 7) / 8 * 8;
+  const bool cut = blockIdx.x >= first;
+  const uint32_t items = cut ? (G.tiles_m * G.tiles_n - G.whole) * G.splits : G.whole;
+  const uint32_t at = cut ? blockIdx.x - first : blockIdx.x, L = at % 8 * ((items + 7) / 8) + at / 8;
+  if (at / 8 >= (items + 7) / 8 || L >= items) return;
+  const uint32_t splits = cut ? G.splits : 1, split = L % splits, tile = (cut ? G.whole : 0) + L / splits;
   const uint32_t band = tile / (8 * G.tiles_n), in = tile % (8 * G.tiles_n);
   const uint32_t height = G.tiles_m - 8 * band < 8 ? G.tiles_m - 8 * band : 8;
   const uint32_t mt = 8 * band + in % height, nt = in / height;
@@ -117,14 +123,14 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
   const uint32_t half = (uint32_t)(P.k >> 1), blocks = (uint32_t)(P.k >> 5);
   const uint32_t sum = (uint32_t)(kBack ? P.n : P.k);  // terms of an output
   const uint32_t steps = (sum + 63) / 64;
-  const uint32_t t0 = (uint32_t)((uint64_t)split * steps / G.splits);
-  const uint32_t t1 = (uint32_t)((uint64_t)(split + 1) * steps / G.splits);
+  const uint32_t t0 = (uint32_t)((uint64_t)split * steps / splits);
+  const uint32_t t1 = (uint32_t)((uint64_t)(split + 1) * steps / splits);
 
   // where a step's slots start, in units: ring slot s
   auto slot_a = [](uint32_t s) { return s * T::A; };
   auto slot_w = [](uint32_t s) { return NS * T::A + s * T::W; };
   auto slot_s = [](uint32_t s) { return NS * (T::A + T::W) + s * T::S; };
-  auto slot_p = [](uint32_t t) { return NS * (T::A + T::W + T::S) + (t & 1) * T::P; };
+  auto slot_r = [](uint32_t t) { return NS * (T::A + T::W + T::S) + (t & 1) * T::R; };  // of step t
   const uint32_t lds0 = lds_address(lds);
 
   // ---- copies: unit `wave * I + i` of 64 of the step's, one 16-byte unit (scales: one byte) a lane.
@@ -159,14 +165,14 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
   };
   auto at_s = [&](int l, int i) {
     const int u = (wave * T::IS + i) * 64 + l;
-    return kBack ? u & 63 : u & 1;
+    return kBack ? u / U : u & 1;
   };
   const uint8_t* wp[T::IW];
 #pragma unroll
   for (int i = 0; i < T::IW; ++i) {
     const int u = (wave * T::IW + i) * 64 + lane;
     if constexpr (kBack) {
-      const uint32_t c = (uint32_t)(n0 >> 5) + ((u % U) ^ swizzle_wt<U>(u / U));
+      const uint32_t c = (uint32_t)(n0 >> 5) + u % U;
       wp[i] = P.w + (int64_t)(u / U) * half + 16 * (int64_t)(c < blocks ? c : blocks - 1);
     } else {
       wp[i] = P.w + weight_row(u >> 1) * half + 16 * at_w(lane, i);
@@ -177,8 +183,8 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
   for (int i = 0; i < T::IS; ++i) {
     const int u = (wave * T::IS + i) * 64 + lane;
     if constexpr (kBack) {
-      const uint32_t c = (uint32_t)(n0 >> 5) + (u >> 6);
-      sp[i] = P.w_scales + (int64_t)(u & 63) * blocks + (c < blocks ? c : blocks - 1);
+      const uint32_t c = (uint32_t)(n0 >> 5) + u % U;
+      sp[i] = P.w_scales + (int64_t)(u / U) * blocks + (c < blocks ? c : blocks - 1);
     } else {
       sp[i] = P.w_scales + weight_row(u >> 1) * blocks + (u & 1);
     }
@@ -187,50 +193,41 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
   auto inside = [&](uint32_t t, int at) {  // row or block `at` of step t lies before the end of the sum
     return kBack ? 64 * t + at < sum : 2 * t + at < blocks;
   };
-  auto copy_scales = [&](uint32_t t, uint32_t s, auto WHOLE) {
-#pragma unroll
-    for (int i = 0; i < T::IS; ++i) {
-      const uint8_t* from = sp[i] + t * step_s;
-      if (!decltype(WHOLE)::value) from = inside(t, at_s(lane, i)) ? from : zeros;
-      copy_byte(from, lds0 + 16 * slot_s(s) + (wave * T::IS + i) * 256);
-    }
-  };
-  // step t to ring slot s (backward: with the scales of step t + 1, to the next slot);
-  // WHOLE: all of it lies before the end of the sum
-  auto copy = [&](uint32_t t, uint32_t s, auto WHOLE) {
+  // the weights and scales of step t to ring slot s; WHOLE: all of it lies before
+  // the end of the sum
+  auto copy_weights = [&](uint32_t t, uint32_t s, auto WHOLE) {
     constexpr bool whole = decltype(WHOLE)::value;
-    const uint32_t to_a = lds0 + 16 * (slot_a(s) + wave * T::IA * 64);
-    const uint32_t to_w = lds0 + 16 * (slot_w(s) + wave * T::IW * 64);
-    const uint8_t* const xs = uniform(xb + (uint64_t)t * 128);
-#pragma unroll
-    for (int i = 0; i < T::IA; ++i) {
-      if constexpr (whole)
-        copy16(xs, xv[i], to_a + i * 1024);
-      else
-        copy16(64 * t + 8 * unit_x(lane, i) < sum ? xs + xv[i] : zeros, to_a + i * 1024);
-    }
 #pragma unroll
     for (int i = 0; i < T::IW; ++i) {
       const uint8_t* from = wp[i] + t * step_w;
       if (!whole) from = inside(t, at_w(lane, i)) ? from : zeros;
-      copy16(from, to_w + i * 1024);
+      copy16(from, lds0 + 16 * (slot_w(s) + (wave * T::IW + i) * 64));
+    }
+#pragma unroll
+    for (int i = 0; i < T::IS; ++i) {
+      const uint8_t* from = sp[i] + t * step_s;
+      if (!whole) from = inside(t, at_s(lane, i)) ? from : zeros;
+      copy_byte(from, lds0 + 16 * slot_s(s) + (wave * T::IS + i) * 256);
+    }
+  };
+  // step t to ring slot s (backward: with the weights of step t + 1, to the next slot)
+  auto copy = [&](uint32_t t, uint32_t s, auto WHOLE) {
+    const uint32_t to_a = lds0 + 16 * (slot_a(s) + wave * T::IA * 64);
+    const uint8_t* const xs = uniform(xb + (uint64_t)t * 128);
+#pragma unroll
+    for (int i = 0; i < T::IA; ++i) {
+      if constexpr (decltype(WHOLE)::value)
+        copy16(xs, xv[i], to_a + i * 1024);
+      else
+        copy16(64 * t + 8 * unit_x(lane, i) < sum ? xs + xv[i] : zeros, to_a + i * 1024);
     }
     if constexpr (kBack)
-      copy_scales(t + 1, s + 1 == NS ? 0 : s + 1, WHOLE);
+      copy_weights(t + 1, s + 1 == NS ? 0 : s + 1, WHOLE);
     else
-      copy_scales(t, s, WHOLE);
+      copy_weights(t, s, WHOLE);
   };
   // steps t that copy() may take as whole
   const uint32_t whole = kBack ? (sum >= 64 ? sum / 64 - 1 : 0) : sum / 64;
-
-  // ---- backward: the scales of step t, in ring slot s, as bytes [block of columns][row]
-  auto turn_scales = [&](uint32_t t, uint32_t s) {
-    if (lane < 16 * T::IS) {
-      const u32x4 v = lds[slot_s(s) + wave * T::IS * 16 + lane];
-      reinterpret_cast<uint32_t*>(lds + slot_p(t))[wave * T::IS * 16 + lane] =
-          v.x | v.y << 8 | v.z << 16 | v.w << 24;
-    }
-  };
 
   f32x16 acc[MT][2];
 #pragma unroll
@@ -240,24 +237,20 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.f;
 
-  // ---- operands.  Of a step: forward the lane's block and scale of each tile,
-  // backward the scales of its 32 rows.  Of a quarter: x, backward the weights.
+  // ---- operands.  Forward, of a step: the lane's block and scale of each tile.
+  // Of a quarter: x, and the weights rebuilt.
   struct Step {
     u32x4 w[2];
     uint32_t s[2];
   };
   struct Quarter {
     u32x4 a[MT];
-    i32x2 w;
   };
   struct Weights {
     u32x4 b[2];
   };
-  auto read_step = [&](Step& v, uint32_t t, uint32_t s) {
-    if constexpr (kBack) {
-#pragma unroll
-      for (int j = 0; j < 2; ++j) v.w[j] = lds[slot_p(t) + (2 * wn + (r >> 4)) * 4 + 2 * h + j];
-    } else {
+  auto read_step = [&](Step& v, uint32_t s) {
+    if constexpr (!kBack) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int row = wn * 64 + 32 * j + r;
@@ -268,87 +261,121 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
   };
   auto read = [&](Quarter& v, uint32_t s, auto Q) {
     constexpr int q = decltype(Q)::value;
-    if constexpr (kBack) {
-      // of the sixteen lanes' addresses, two neighbours give a row's 16 bytes
-      const int p = lane & 15, row = 32 * h + 8 * q + (p >> 1);
-      const int unit = (2 * wn + ((lane >> 4) & 1)) ^ swizzle_wt<U>(row);
-      const uint8_t* const at = reinterpret_cast<const uint8_t*>(lds + slot_w(s) + row * U + unit) + 8 * (p & 1);
-      v.w = __builtin_amdgcn_ds_read_tr8_b64_v2i32((__attribute__((address_space(3))) i32x2*)at);
-    }
 #pragma unroll
     for (int i = 0; i < MT; ++i) {
       const int row = wm * (32 * MT) + 32 * i + r;
       v.a[i] = lds[slot_a(s) + 8 * row + ((4 * h + q) ^ swizzle_x(row))];
     }
   };
-  // a scale byte b at the conversion: its operand's exponent field (it reads no
-  // other bit; 0 stands for 2^-127 there, 255 gives NaN)
-  auto pair = [](uint32_t d, uint32_t scale, auto SEL) {
-    return __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(
-                                            d, __builtin_bit_cast(float, scale), decltype(SEL)::value));
+  // Eight values of a dword at a scale byte: the conversion takes the exponent
+  // field of its scale and no other bit (0 stands for 2^-127 there, 255 gives NaN).
+  auto rebuild8 = [](uint32_t d, uint32_t scale) {
+    const float s = __builtin_bit_cast(float, scale << 23);
+    return (u32x4){__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 0)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 1)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 2)),
+                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 3))};
   };
-  auto rebuild = [&](Weights& v, const Step& st, const Quarter& o, auto Q) {
+  // a quarter's weights of step t: forward rebuilt, backward read as they were rebuilt
+  auto weights = [&](Weights& v, const Step& st, uint32_t t, auto Q) {
     constexpr int q = decltype(Q)::value;
-    using I0 = std::integral_constant<int, 0>;
-    using I1 = std::integral_constant<int, 1>;
-    using I2 = std::integral_constant<int, 2>;
-    using I3 = std::integral_constant<int, 3>;
-    if constexpr (kBack) {
 #pragma unroll
-      for (int d = 0; d < 2; ++d) {  // four rows: scale bytes 8 q + 4 d .. + 3
-        const uint32_t s = st.w[q >> 1][2 * (q & 1) + d], w = (uint32_t)o.w[d];
-        const uint32_t p0 = pair(w, s << 23, I0{}), p1 = pair(w, s << 15, I1{});
-        const uint32_t p2 = pair(w, s << 7, I2{}), p3 = pair(w, s >> 1, I3{});
-        v.b[0][2 * d] = perm(p1, p0, 0x05040100u);
-        v.b[0][2 * d + 1] = perm(p3, p2, 0x05040100u);
-        v.b[1][2 * d] = perm(p1, p0, 0x07060302u);
-        v.b[1][2 * d + 1] = perm(p3, p2, 0x07060302u);
-      }
-    } else {
+    for (int j = 0; j < 2; ++j) {
+      if constexpr (kBack) {
+        // sixteen lanes' addresses are four rows of four eight-byte pieces
+        const int p = lane & 15, c = wn * 64 + 32 * j + 16 * ((lane >> 4) & 1) + 4 * (p & 3);
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        const uint32_t d = st.w[j][q], s = st.s[j] << 23;
-        v.b[j] = (u32x4){pair(d, s, I0{}), pair(d, s, I1{}), pair(d, s, I2{}), pair(d, s, I3{})};
+        for (int d = 0; d < 2; ++d) {
+          const int row = 32 * h + 8 * q + 4 * d + (p >> 2);
+          const u32x4* const at = lds + slot_r(t) + row * (T::BN / 8) + swizzle_r<T::BN>(row, c >> 3);
+          const u32x2 x = __builtin_bit_cast(
+              u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+                         (__attribute__((address_space(3))) i16x4*)(reinterpret_cast<const u32x2*>(at) + (p & 1))));
+          v.b[j][2 * d] = x.x;
+          v.b[j][2 * d + 1] = x.y;
+        }
+      } else {
+        v.b[j] = rebuild8(st.w[j][q], st.s[j]);
       }
     }
   };
+  // ---- backward: the weights of step t, in ring slot s, rebuilt to rows of bf16.
+  // A wave takes the units that it copied itself: 32 values of one row and block.
+  struct Unit {
+    u32x4 w;
+    uint32_t s;
+  };
+  auto read_unit = [&](Unit& v, uint32_t s, int i) {
+    const int u = (wave * T::IW + i) * 64 + lane;
+    v.w = lds[slot_w(s) + u];
+    v.s = reinterpret_cast<const uint32_t*>(lds + slot_s(s))[u];
+  };
+  auto rebuild_unit = [&](const Unit& v, uint32_t t, int i) {
+    const int u = (wave * T::IW + i) * 64 + lane, row = u / U, c = u % U;
+#pragma unroll
+    for (int e = 0; e < 4; ++e)
+      lds[slot_r(t) + row * (T::BN / 8) + swizzle_r<T::BN>(row, 4 * c + e)] = rebuild8(v.w[e], v.s);
+  };
+  auto multiply_row = [&](const Quarter& o, const Weights& v, int i) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) acc[i][j] = mfma32x32x16(o.a[i], v.b[j], acc[i][j]);
+  };
   auto multiply = [&](const Quarter& o, const Weights& v) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+    for (int i = 0; i < MT; ++i) multiply_row(o, v, i);
+  };
+  // A quarter's products with the next one's reads and rebuilding between them:
+  // left alone, the compiler puts the reads behind the products and waits for
+  // them before the next.
+  auto interleave = [&]() {
+    constexpr int products = 2 * MT, reads = MT + (kBack ? 4 : 0), valu = 8 / products + 1;
 #pragma unroll
-      for (int j = 0; j < 2; ++j) acc[i][j] = mfma32x32x16(o.a[i], v.b[j], acc[i][j]);
+    for (int n = 0; n < products; ++n) {
+#pragma unroll
+      for (int m = n * reads / products; m < (n + 1) * reads / products; ++m)
+        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+      __builtin_amdgcn_sched_group_barrier(0x002, valu, 0);
+    }
+    __builtin_amdgcn_sched_barrier(0);
   };
   using Q0 = std::integral_constant<int, 0>;
   using Q1 = std::integral_constant<int, 1>;
   using Q2 = std::integral_constant<int, 2>;
   using Q3 = std::integral_constant<int, 3>;
 
-  // ---- the loop.  A quarter's operands are read while the one before is
-  // multiplied.  The barrier of a step comes before its last quarter: by then
-  // every wave holds that in registers, so the step's slot can take the copies
-  // of step t + NS, and the next step's first operands are read, while it is
-  // multiplied.
+  // ---- the loop.  A quarter's operands are read and rebuilt while the one before
+  // is multiplied, backward the next step's weights too, a unit a quarter.  The
+  // barrier of a step comes before its last quarter: by then every wave holds that
+  // in registers, so the step's slot can take the copies of step t + NS, and the
+  // next step's first operands are read, while it is multiplied.
+  static_assert(T::IW <= 2, "a unit in each of the first two quarters");
   Step st;
   Quarter o0, o1;
-  Weights b;
+  Weights b0, b1;
+  Unit unit;
   uint32_t cur = t0 % NS;
   auto step = [&](uint32_t t, auto FAST) {
     constexpr bool fast = decltype(FAST)::value;  // step t + NS exists and is whole
     const uint32_t next = cur + 1 == NS ? 0 : cur + 1;
-    if constexpr (kBack) turn_scales(t + 1, next);
+    if constexpr (kBack) read_unit(unit, next, 0);
     read(o1, cur, Q1{});
-    rebuild(b, st, o0, Q0{});
-    multiply(o0, b);
-    __builtin_amdgcn_sched_barrier(0);
+    weights(b1, st, t, Q1{});
+    multiply(o0, b0);
+    interleave();
+    if constexpr (kBack) {
+      rebuild_unit(unit, t + 1, 0);
+      if constexpr (T::IW > 1) read_unit(unit, next, 1);
+    }
     read(o0, cur, Q2{});
-    rebuild(b, st, o1, Q1{});
-    multiply(o1, b);
-    __builtin_amdgcn_sched_barrier(0);
+    weights(b0, st, t, Q2{});
+    multiply(o1, b1);
+    interleave();
+    if constexpr (kBack && T::IW > 1) rebuild_unit(unit, t + 1, 1);
     read(o1, cur, Q3{});
-    rebuild(b, st, o0, Q2{});
-    multiply(o0, b);
-    rebuild(b, st, o1, Q3{});
-    __builtin_amdgcn_sched_barrier(0);
+    weights(b1, st, t, Q3{});
+    multiply(o0, b0);
+    interleave();
     // the last operands (on every path here: after the branch the compiler's
     // own wait would be for the next step's reads too)
     __builtin_amdgcn_s_waitcnt(kWaitLds);
@@ -359,31 +386,41 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
       else
         __builtin_amdgcn_s_waitcnt(wait_vm(0));
       lds_barrier();
-      if constexpr (fast) {
-        copy(t + NS, cur, std::true_type{});
-      } else {
-        if (t + NS < t1) copy(t + NS, cur, std::false_type{});
-      }
-      read_step(st, t + 1, next);
+      read_step(st, next);
       read(o0, next, Q0{});
+      if constexpr (kBack) weights(b0, st, t + 1, Q0{});
+      __builtin_amdgcn_sched_barrier(0);
+      if constexpr (!fast) {
+        if (t + NS < t1) copy(t + NS, cur, std::false_type{});
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
+    multiply_row(o1, b1, 0);
     __builtin_amdgcn_sched_barrier(0);
-    multiply(o1, b);
+    if constexpr (fast) copy(t + NS, cur, std::true_type{});
     __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 1; i < MT; ++i) multiply_row(o1, b1, i);
+    __builtin_amdgcn_sched_barrier(0);
+    if constexpr (!kBack) weights(b0, st, t + 1, Q0{});  // (of no step, behind the last)
     cur = next;
   };
-  if constexpr (kBack) copy_scales(t0, cur, std::false_type{});
+  if constexpr (kBack) copy_weights(t0, cur, std::false_type{});
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
     if (kBack && i == NS - 1) {
-      // this step's copies bring scales to the slot of t0's, which are turned
-      // first (behind a barrier: nothing else keeps their reads below the wait)
+      // these copies bring weights to the slot of t0's, which are rebuilt first
+      // (behind a barrier: nothing else keeps their reads below the wait)
       if (t0 + NS - 1 <= t1)
         __builtin_amdgcn_s_waitcnt(wait_vm((NS - 1) * T::COPIES));
       else
         __builtin_amdgcn_s_waitcnt(wait_vm(0));
       lds_barrier();
-      turn_scales(t0, cur);
+#pragma unroll
+      for (int j = 0; j < T::IW; ++j) {
+        read_unit(unit, cur, j);
+        rebuild_unit(unit, t0, j);
+      }
       __builtin_amdgcn_s_waitcnt(kWaitLds);
       lds_barrier();
     }
@@ -394,12 +431,76 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
   else
     __builtin_amdgcn_s_waitcnt(wait_vm(0));
   lds_barrier();
-  read_step(st, t0, cur);
+  read_step(st, cur);
   read(o0, cur, Q0{});
+  weights(b0, st, t0, Q0{});
   const uint32_t tw = whole < t1 ? whole : t1;  // steps t with t + NS < tw are fast
   uint32_t t = t0;
   for (; t + NS < tw; ++t) step(t, std::true_type{});
   for (; t < t1; ++t) step(t, std::false_type{});
+
+  // ---- a part's sums: written, and by the last one of the tile's parts added in
+  // order (the same bits whichever is last).  They are written and read with
+  // device scope, past the caches that belong to one XCD, so that a wave's wait
+  // for its stores is all that the count needs before it: a release of the device
+  // would write back an XCD's whole cache (13 against 9 us on a call of one row).
+  if (splits > 1) {
+    constexpr int kPairs = MT * 2 * 8;  // of a thread
+    uint64_t* const parts = G.partial + (uint64_t)(tile - G.whole) * splits * (kPairs * T::THREADS) + tid;
+    uint64_t* const mine = parts + (uint64_t)split * (kPairs * T::THREADS);
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          const f32x2 x = {acc[i][j][2 * v], acc[i][j][2 * v + 1]};
+          __hip_atomic_store(mine + ((i * 2 + j) * 8 + v) * T::THREADS, __builtin_bit_cast(uint64_t, x), __ATOMIC_RELAXED,
+                             __HIP_MEMORY_SCOPE_AGENT);
+        }
+    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+    __shared__ uint32_t before;
+    __syncthreads();
+    if (tid == 0) {
+      uint32_t* const c = G.counted + (tile - G.whole);
+      before = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+      if (before + 1 == splits) __hip_atomic_store(c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    }
+    __syncthreads();
+    if (before + 1 != splits) return;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        f32x2 total[8];
+        for (uint32_t p0 = 0; p0 < splits; p0 += 4) {  // (eight pairs of four parts in flight)
+          uint64_t x[4][8];
+#pragma unroll
+          for (uint32_t p = 0; p < 4; ++p)
+            if (p0 + p < splits) {
+#pragma unroll
+              for (int v = 0; v < 8; ++v)
+                x[p][v] = __hip_atomic_load(parts + (uint64_t)(p0 + p) * (kPairs * T::THREADS) + ((i * 2 + j) * 8 + v) * T::THREADS,
+                                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            }
+#pragma unroll
+          for (uint32_t p = 0; p < 4; ++p)
+            if (p0 + p < splits) {
+#pragma unroll
+              for (int v = 0; v < 8; ++v) {
+                const f32x2 y = __builtin_bit_cast(f32x2, x[p][v]);
+                total[v].x = p0 + p == 0 ? y.x : total[v].x + y.x;
+                total[v].y = p0 + p == 0 ? y.y : total[v].y + y.y;
+              }
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < 8; ++v) {
+          acc[i][j][2 * v] = total[v].x;
+          acc[i][j][2 * v + 1] = total[v].y;
+        }
+      }
+  }
 
   // ---- outputs.  D[row of x][column]: lane half h, register q hold row
   // 8 (q / 4) + 4 h + q % 4 of column r.  Stores go through a resource that ends
@@ -447,17 +548,10 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
                                                 at + row_of(i, q) * pitch, 0, 0);
     }
   };
-  const bool part = G.partial != nullptr;
   if constexpr (kGate) {
     const int c = wn * 32 + r;
     auto gate = [&](int i, int q) -> float { return acc[i][0][q]; };
     auto up = [&](int i, int q) -> float { return acc[i][1][q]; };
-    if (part) {
-      float* const p = G.partial + (int64_t)split * P.m * 2 * N;
-      put_f32(resource(p, 2 * N, n0, 4), (uint32_t)N * 8, c, gate);
-      put_f32(resource(p, 2 * N, N + n0, 4), (uint32_t)N * 8, c, up);
-      return;
-    }
     const bool even = (N & 1) == 0;
     if (P.gu) {
       const bool pairs = even && (reinterpret_cast<uintptr_t>(P.gu) & 3) == 0;
@@ -475,12 +569,23 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
     else
       put_f32(resource(P.y, N, n0, 4), (uint32_t)N * 4, c, gate);
   } else {
-    const int c = wn * 64 + 2 * r;
-    void* const y = part ? G.partial + (int64_t)split * P.m * N : P.y;
-    const int size = P.y_bf16 && !part ? 2 : 4;
-    const __amdgpu_buffer_rsrc_t d = resource(y, N, n0, size);
+    const int size = P.y_bf16 ? 2 : 4;
+    const __amdgpu_buffer_rsrc_t d = resource(P.y, N, n0, size);
     const uint32_t pitch = (uint32_t)N * size;
-    if (size == 2 && (N & 1) == 0 && (reinterpret_cast<uintptr_t>(y) & 3) == 0) {
+    const bool pairs = (N & 1) == 0 && (reinterpret_cast<uintptr_t>(P.y) & 3) == 0;
+    if constexpr (kBack) {  // tile j's columns 32 j + r
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        auto value = [&](int i, int q) -> float { return acc[i][j][q]; };
+        if (size == 2)
+          put_bf16(d, pitch, wn * 64 + 32 * j + r, pairs, value);
+        else
+          put_f32(d, pitch, wn * 64 + 32 * j + r, value);
+      }
+      return;
+    }
+    const int c = wn * 64 + 2 * r;
+    if (size == 2 && pairs) {
       const uint32_t at = c < cols_n ? (uint32_t)row0 * pitch + 2u * c : kStoreOOB;
 #pragma unroll
       for (int i = 0; i < MT; ++i)
@@ -507,34 +612,6 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
   }
 }
 
-// y = the sum of the parts in order (gated: act(g) * u of the sums, and gu), one
-// row's values of four columns a thread.
-template <bool GATE>
-__global__ __launch_bounds__(256) void mx_bf16_join_kernel(MxBf16Problem P, const float* __restrict__ partial,
-                                                           uint32_t splits, int64_t N, int64_t count) {
-  const int64_t first = ((int64_t)blockIdx.x * 256 + threadIdx.x) * 4;
-  const int64_t part = P.m * N * (GATE ? 2 : 1);
-  for (int64_t j = first; j < first + 4 && j < count; ++j) {
-    int64_t at = j;
-    if constexpr (GATE) at = j + j / N * N;  // row j / N of 2 N
-    float v = partial[at];
-    for (uint32_t s = 1; s < splits; ++s) v += partial[s * part + at];
-    if constexpr (GATE) {
-      float u = partial[at + N];
-      for (uint32_t s = 1; s < splits; ++s) u += partial[s * part + at + N];
-      if (P.gu) {
-        P.gu[at] = (uint16_t)f32_to_bf16_bits(v);
-        P.gu[at + N] = (uint16_t)f32_to_bf16_bits(u);
-      }
-      with_activation(P.act, [&](auto ACT) { v = activate<decltype(ACT)::value>(v) * u; });
-    }
-    if (P.y_bf16)
-      reinterpret_cast<uint16_t*>(P.y)[j] = (uint16_t)f32_to_bf16_bits(v);
-    else
-      reinterpret_cast<float*>(P.y)[j] = v;
-  }
-}
-
 int device_cus() {
   int dev = 0, cus = 256;
   if (hipGetDevice(&dev) != hipSuccess ||
@@ -554,29 +631,35 @@ auto with_tile(int tile, F&& f) {
   }
 }
 
+// tiles_m * tiles_n tiles, the first `whole` unsplit, the others in `splits` parts.
 struct Plan {
   int tile;
   uint32_t splits;
-  int64_t tiles_m, tiles_n;
-  int64_t blocks() const { return (tiles_m * tiles_n * splits + 7) / 8 * 8; }
+  int64_t tiles_m, tiles_n, whole;
+  int64_t cut() const { return tiles_m * tiles_n - whole; }
+  int64_t blocks() const { return (whole + 7) / 8 * 8 + (cut() * splits + 7) / 8 * 8; }
 };
 
 int64_t outputs(const MxBf16Problem& p) { return p.kind == kMxBackward ? p.k : p.n; }
 int64_t steps_of(const MxBf16Problem& p) { return ((p.kind == kMxBackward ? p.n : p.k) + 63) / 64; }
 
-// Tile number t with the sum in s parts; tile < 0 where they do not fit the
-// problem: a tile's rows of x and of outputs stay below 2^31 bytes, each part has
-// a step, and a launch holds the blocks (of the join, too).
+// Tiles that are cut at most: their counts have a place of their own.
+constexpr int64_t kMaxCut = kMxCounters;
+
+// Tile number t, the tiles from `whole` on in s parts (s == 1: none); tile < 0
+// where they do not fit the problem: a tile's rows of x and of outputs stay below
+// 2^31 bytes, each part has a step, and a launch holds the blocks.
 template <typename T>
-Plan plan_on(const MxBf16Problem& p, int t, uint32_t s) {
+Plan plan_on(const MxBf16Problem& p, int t, uint32_t s, int64_t whole) {
   const int64_t N = outputs(p), wide = p.kind == kMxGated ? 2 * N : N;
   const int64_t cols = p.kind == kMxGated ? T::BN / 2 : T::BN;
-  Plan q{t, s, (p.m + T::BM - 1) / T::BM, (N + cols - 1) / cols};
+  Plan q{t, s, (p.m + T::BM - 1) / T::BM, (N + cols - 1) / cols, whole};
+  const int64_t tiles = q.tiles_m * q.tiles_n;
+  if (s == 1) q.whole = tiles;
   constexpr int64_t kTileBytes = (INT64_C(1) << 31) - 1;
   if (4 * wide > kTileBytes / T::BM || 2 * p.x_pitch > kTileBytes / T::BM) q.tile = -1;
-  if ((int64_t)s > steps_of(p)) q.tile = -1;
-  if ((q.tiles_m * q.tiles_n * s + 7) * T::THREADS > kMaxLaunchThreads) q.tile = -1;
-  if (s > 1 && (p.m * N + 1023) / 1024 * 256 > kMaxLaunchThreads) q.tile = -1;
+  if (q.whole > tiles || (int64_t)s > steps_of(p) || (s > 1 && q.cut() > kMaxCut)) q.tile = -1;
+  if ((tiles * s + 14) * T::THREADS > kMaxLaunchThreads) q.tile = -1;
   return q;
 }
 
@@ -586,32 +669,37 @@ struct Cost {
   float first, step;
   int per_cu;
 };
-constexpr Cost kCost[kTiles] = {{7.0f, 1.05f, 1}, {4.0f, 0.60f, 1}, {3.0f, 0.38f, 1}, {2.5f, 0.28f, 1}, {2.0f, 0.22f, 1}};
+constexpr Cost kCost[kTiles] = {{7.0f, 1.55f, 1}, {4.0f, 0.90f, 1}, {3.0f, 0.55f, 1}, {2.5f, 0.40f, 1}, {2.0f, 0.35f, 1}};
 
 Plan make_plan(const MxBf16Problem& p) {
   const int64_t cus = device_cus();
-  Plan best{4, 1, 0, 0};
+  Plan best{4, 1, 0, 0, 0};
   double least = 0;
   for (int t = 0; t < kTiles; ++t)
-    for (uint32_t s = 1; s <= kMaxSplits; s *= 2) {
-      const Plan q = with_tile(t, [&](auto X) { return plan_on<decltype(X)>(p, t, s); });
-      if (q.tile < 0) continue;
-      const int64_t n = q.tiles_m * q.tiles_n * s;
-      const double k = (double)((steps_of(p) + s - 1) / s);
-      double us = (double)((n + cus - 1) / cus) * (kCost[t].first + kCost[t].step * k);
-      if (s > 1) us += 3.0 + (double)s * p.m * outputs(p) * 8 / 4e6;
-      if (best.tiles_m == 0 || us < least) {
-        least = us;
-        best = q;
+    with_tile(t, [&](auto X) {
+      for (uint32_t s : {1u, 2u, 3u, 4u, 6u, 8u, 12u, 16u}) {
+        Plan q = plan_on<decltype(X)>(p, t, s, 0);
+        const int64_t tiles = q.tiles_m * q.tiles_n;
+        if (s > 1 && tiles > cus) q = plan_on<decltype(X)>(p, t, s, tiles / cus * cus);
+        if (q.tile < 0) continue;
+        const double k = (double)steps_of(p), part = (double)((steps_of(p) + s - 1) / s);
+        double us = (double)((q.whole + cus - 1) / cus) * (kCost[t].first + kCost[t].step * k);
+        if (s > 1)
+          us += (double)((q.cut() * s + cus - 1) / cus) * (kCost[t].first + kCost[t].step * part) + 3.0 +
+                s * decltype(X)::BM * decltype(X)::BN * 4 / 50000.0;
+        if (best.tiles_m == 0 || us < least) {
+          least = us;
+          best = q;
+        }
       }
-    }
-  if (best.tiles_m == 0) best.tiles_m = best.tiles_n = INT64_C(1) << 31;  // too many tiles of every size
+    });
+  if (best.tiles_m == 0) best.tiles_m = best.tiles_n = best.whole = INT64_C(1) << 31;  // too many tiles of every size
   return best;
 }
 
 template <int KIND, typename T>
 hipError_t launch_tile(const MxBf16Problem& p, const GemmArgs& g, uint32_t blocks, hipStream_t stream) {
-  constexpr int lds = T::LDS * 16;
+  constexpr int lds = 16 * (KIND == kMxBackward ? T::BACKWARD : T::FORWARD);
   // the LDS limit is raised once per device (one bit each for the first 64);
   // callers racing here all set the same value
   static std::atomic<uint64_t> configured{0};
@@ -629,37 +717,65 @@ hipError_t launch_tile(const MxBf16Problem& p, const GemmArgs& g, uint32_t block
   return hipGetLastError();
 }
 
-hipError_t launch_plan(const MxBf16Problem& p, const Plan& q, float* partial, hipStream_t stream) {
-  const GemmArgs g{(uint32_t)q.tiles_m, (uint32_t)q.tiles_n, q.splits, q.splits > 1 ? partial : nullptr};
-  const hipError_t e = with_tile(q.tile, [&](auto X) {
+// The workspace: the caller's `reserve` bytes (whole 256), then the parts' sums.
+template <typename F>
+hipError_t launch_plan(const MxBf16Problem& problem, const Plan& q, size_t reserve, hipStream_t stream, F&& fill) {
+  MxBf16Problem p = problem;
+  GemmArgs g{(uint32_t)q.tiles_m, (uint32_t)q.tiles_n, (uint32_t)q.whole, q.splits, nullptr, nullptr};
+  return with_tile(q.tile, [&](auto X) -> hipError_t {
     using T = decltype(X);
+    const size_t bytes = reserve + (q.splits > 1 ? (size_t)q.cut() * q.splits * T::BM * T::BN * sizeof(float) : 0);
+    char* ws = nullptr;
+    hipError_t e = bytes ? stream_workspace(kWorkspaceMx, stream, bytes, &ws) : hipSuccess;
+    if (e == hipSuccess && q.splits > 1) e = stream_counters(stream, &g.counted);
+    if (e == hipSuccess) e = fill(p, ws);
+    if (e != hipSuccess) return e;
+    g.partial = reinterpret_cast<uint64_t*>(ws + reserve);
     const uint32_t blocks = (uint32_t)q.blocks();
     if (p.kind == kMxGated) return launch_tile<kMxGated, T>(p, g, blocks, stream);
     if (p.kind == kMxBackward) return launch_tile<kMxBackward, T>(p, g, blocks, stream);
     return launch_tile<kMxForward, T>(p, g, blocks, stream);
   });
-  if (e != hipSuccess || q.splits == 1) return e;
-  const int64_t N = outputs(p), count = p.m * N;
-  const dim3 grid((uint32_t)((count + 1023) / 1024));
-  if (p.kind == kMxGated)
-    mx_bf16_join_kernel<true><<<grid, dim3(256), 0, stream>>>(p, partial, q.splits, N, count);
-  else
-    mx_bf16_join_kernel<false><<<grid, dim3(256), 0, stream>>>(p, partial, q.splits, N, count);
-  return hipGetLastError();
-}
-
-size_t partial_bytes(const MxBf16Problem& p, const Plan& q) {
-  return q.splits == 1 ? 0 : (size_t)q.splits * p.m * outputs(p) * (p.kind == kMxGated ? 2 : 1) * sizeof(float);
 }
 
 }  // namespace
 
-bool mx_bf16_fits(const MxBf16Problem& p) { return make_plan(p).blocks() <= 0x7FFFFFFF; }
+bool mx_bf16_fits(const MxBf16Problem& p) {
+  // No tile is smaller than 32 x 64 outputs or has more than 512 threads: where a
+  // launch holds the blocks of that, it holds any plan's, and the costs are
+  // computed by the launch only.
+  if (((p.m + 31) / 32 * ((outputs(p) + 63) / 64) * kMaxSplits + 14) * 512 <= kMaxLaunchThreads) return true;
+  return make_plan(p).blocks() <= 0x7FFFFFFF;
+}
 
-size_t mx_bf16_workspace_bytes(const MxBf16Problem& p) { return partial_bytes(p, make_plan(p)); }
+hipError_t launch_mx_bf16_with(const MxBf16Problem& p, size_t reserve, MxBf16Fill* fill, hipStream_t stream) {
+  return launch_plan(p, make_plan(p), reserve, stream, [&](MxBf16Problem& on, char* ws) {
+    return fill ? (*fill)(on, ws) : hipSuccess;
+  });
+}
 
-hipError_t launch_mx_bf16_on(const MxBf16Problem& p, char* ws, hipStream_t stream) {
-  return launch_plan(p, make_plan(p), reinterpret_cast<float*>(ws), stream);
+extern "C" int32_t w4_mx_bf16_kernel_of(int32_t kind, int64_t n, int64_t k, int64_t m) {
+  const MxBf16Problem p{nullptr, nullptr, nullptr, nullptr, nullptr, m, n, k, kind == kMxBackward ? n : k, 0, 0, kind};
+  const Plan q = make_plan(p);
+  return (q.whole > 0 && q.splits > 1 ? 1024 : 0) + 16 * (int32_t)q.splits + q.tile;
+}
+
+extern "C" int32_t w4_mx_bf16_product_on(int32_t kernel, int32_t kind, int32_t act, int64_t n, int64_t k,
+                                         const uint8_t* w, const uint8_t* w_scales, const uint16_t* x, int64_t m,
+                                         uint16_t* gu, void* y, int32_t y_bf16, void* stream) {
+  const MxBf16Problem p{w, w_scales, x, y, gu, m, n, k, kind == kMxBackward ? n : k, y_bf16, act, kind};
+  if (kind < kMxForward || kind > kMxBackward || (kind == kMxBackward && n % 8)) return hipErrorInvalidValue;
+  const int32_t parts = kernel % 1024 / 16, tile = kernel % 16;
+  if (kernel < 0 || kernel >= 2048 || tile >= kTiles || parts < 1 || parts > (int32_t)kMaxSplits)
+    return hipErrorInvalidValue;
+  const Plan q = with_tile(tile, [&](auto X) {
+    const Plan all = plan_on<decltype(X)>(p, tile, (uint32_t)parts, 0);
+    if (kernel < 1024) return all;
+    const int64_t tiles = all.tiles_m * all.tiles_n, cus = device_cus();
+    return plan_on<decltype(X)>(p, tile, (uint32_t)parts, tiles > cus ? tiles / cus * cus : tiles / 2 / 8 * 8);
+  });
+  if (q.tile < 0) return hipErrorInvalidValue;
+  return launch_plan(p, q, 0, static_cast<hipStream_t>(stream), [](MxBf16Problem&, char*) { return hipSuccess; });
 }
 
 }  // namespace w4

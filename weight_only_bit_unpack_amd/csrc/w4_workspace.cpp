@@ -20,17 +20,12 @@
 #include <tuple>
 
 namespace w4 {
-namespace {
 
-// A number of the calling thread from 1 on, never given again (the system gives
-// an ended thread's id again, while its last kernels may still run).
 uint64_t this_thread() {
   static std::atomic<uint64_t> threads{0};
   thread_local const uint64_t id = ++threads;
   return id;
 }
-
-}  // namespace
 
 hipError_t stream_workspace(int user, hipStream_t stream, size_t bytes, char** out) {
   static std::mutex mu;
