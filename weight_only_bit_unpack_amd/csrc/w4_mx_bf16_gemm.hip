@@ -34,27 +34,30 @@ namespace {
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 
 // A block of BM rows of x by BN columns (forward: weight rows): WM x WN waves,
-// each with MT x 2 accumulators of 32 x 32.  NS (backward: NB) steps of 64 in LDS:
-// one read, the others arriving.
-template <int BM_, int BN_, int WM_, int WN_, int NS_, int NB_>
+// each with MT x 2 accumulators of 32 x 32, and WK groups of such waves that take
+// the steps of 64 in turn, each with LDS of its own: where there are too few
+// tiles to give a SIMD two waves otherwise, its instructions' latencies are the
+// bound.  NS (backward: NB) steps of a group in LDS: one read, the others arriving.
+template <int BM_, int BN_, int WM_, int WN_, int WK_, int NS_, int NB_>
 struct Tile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, NS = NS_, NB = NB_;
-  static constexpr int NW = WM * WN, THREADS = 64 * NW, MT = BM / WM / 32;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, WK = WK_, NS = NS_, NB = NB_;
+  static constexpr int NW = WM * WN, THREADS = 64 * NW * WK, MT = BM / WM / 32;
   static_assert(BN == 64 * WN && BM == 32 * WM * MT, "waves of 32 MT x 64");
   // 16-byte units of a step: rows of x, weights, scale bytes (a dword each)
   static constexpr int A = BM * 8, W = BN * 2, S = BN / 2;
   static constexpr int R = BN * 8;  // backward: 64 rows of BN rebuilt weights
-  static constexpr int IA = A / THREADS, IW = W / THREADS, IS = 4 * S / THREADS;  // copies of a wave
-  static_assert(IA * THREADS == A && IW * THREADS == W && IS * THREADS == 4 * S, "the waves share the copies");
+  static constexpr int IA = A / (64 * NW), IW = W / (64 * NW), IS = 4 * S / (64 * NW);  // copies of a wave
+  static_assert(IA * 64 * NW == A && IW * 64 * NW == W && IS == IW, "the waves share the copies");
   static constexpr int COPIES = IA + IW + IS;
-  static constexpr int FORWARD = NS * (A + W + S), BACKWARD = NB * (A + W + S) + 2 * R;  // units of LDS
-  static_assert(FORWARD <= 10240 && BACKWARD <= 10240, "the LDS of a CU");
+  static constexpr int FORWARD = NS * (A + W + S), BACKWARD = NB * (A + W + S) + 2 * R;  // units of a group's LDS
+  static_assert(WK * FORWARD < 10240 && WK * BACKWARD < 10240, "the LDS of a CU");
+  static_assert((WK - 1) * BM * BN / 4 <= WK * FORWARD, "the groups' sums fit in it");
 };
-using T0 = Tile<256, 256, 2, 4, 3, 2>;
-using T1 = Tile<128, 256, 2, 4, 3, 3>;
-using T2 = Tile<128, 128, 2, 2, 3, 2>;
-using T3 = Tile<64, 128, 2, 2, 3, 3>;
-using T4 = Tile<32, 128, 1, 2, 3, 2>;
+using T0 = Tile<256, 256, 2, 4, 1, 3, 2>;
+using T1 = Tile<128, 256, 2, 4, 1, 3, 3>;
+using T2 = Tile<128, 128, 2, 2, 2, 3, 2>;
+using T3 = Tile<64, 128, 2, 2, 2, 3, 2>;
+using T4 = Tile<32, 64, 1, 1, 4, 3, 2>;
 constexpr int kTiles = 5;
 
 constexpr uint32_t kMaxSplits = 16;
@@ -86,8 +89,10 @@ __device__ __forceinline__ int swizzle_w(int row) { return (row >> 3) & 1; }
 // (32 lanes: four rows, four units each) both take all of the banks' units.
 template <int BN>
 __device__ __forceinline__ int swizzle_r(int row, int c) {
-  const int n0 = row & 1, n1 = (row >> 1) & 1;
-  return c ^ (n1 << 3 | n0 << 2 | (n0 ^ ((c >> 3) & 1)) << 1 | (BN == 256 ? (c >> 4) & 1 : n1));
+  const int n0 = row & 1, n1 = (row >> 1) & 1, c3 = (c >> 3) & 1, c4 = (c >> 4) & 1;
+  if constexpr (BN == 256) return c ^ (n1 << 3 | n0 << 2 | (n0 ^ c3) << 1 | c4);
+  if constexpr (BN == 128) return c ^ (n1 << 3 | n0 << 2 | (n0 ^ c3) << 1 | n1);
+  return c ^ (n1 << 2 | n1 << 1 | n0);
 }
 
 template <int KIND, typename T>
@@ -98,7 +103,8 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
   constexpr int OUT = kGate ? T::BN / 2 : T::BN;       // outputs of a row in the tile
   extern __shared__ u32x4 lds[];
   const int tid = threadIdx.x, lane = tid & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int waves = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wave = waves % T::NW, group = waves / T::NW;  // of the group
   const int wm = wave % T::WM, wn = wave / T::WM;
   const int r = lane & 31, h = lane >> 5;
 
@@ -121,16 +127,21 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
   const int rows_m = (int)(P.m - m0 < T::BM ? P.m - m0 : T::BM);
   const int cols_n = (int)(N - n0 < OUT ? N - n0 : OUT);
   const uint32_t half = (uint32_t)(P.k >> 1), blocks = (uint32_t)(P.k >> 5);
-  const uint32_t sum = (uint32_t)(kBack ? P.n : P.k);  // terms of an output
-  const uint32_t steps = (sum + 63) / 64;
+  // this part's steps of 64 terms, t0 .. t1 - 1, of which the group takes every
+  // WK-th; `count` each (a group's last may lie behind t1: zeros)
+  const uint32_t terms = (uint32_t)(kBack ? P.n : P.k), steps = (terms + 63) / 64;
   const uint32_t t0 = (uint32_t)((uint64_t)split * steps / splits);
   const uint32_t t1 = (uint32_t)((uint64_t)(split + 1) * steps / splits);
+  const uint32_t end = split + 1 == splits ? terms : 64 * t1;  // of the part's terms
+  const uint32_t count = (t1 - t0 + T::WK - 1) / T::WK;
+  auto step_at = [&](uint32_t i) { return t0 + group + T::WK * i; };
 
-  // where a step's slots start, in units: ring slot s
-  auto slot_a = [](uint32_t s) { return s * T::A; };
-  auto slot_w = [](uint32_t s) { return NS * T::A + s * T::W; };
-  auto slot_s = [](uint32_t s) { return NS * (T::A + T::W) + s * T::S; };
-  auto slot_r = [](uint32_t t) { return NS * (T::A + T::W + T::S) + (t & 1) * T::R; };  // of step t
+  // where a step's slots start, in units: ring slot s, the rebuilt weights of step i
+  const uint32_t base = group * (kBack ? T::BACKWARD : T::FORWARD);
+  auto slot_a = [&](uint32_t s) { return base + s * T::A; };
+  auto slot_w = [&](uint32_t s) { return base + NS * T::A + s * T::W; };
+  auto slot_s = [&](uint32_t s) { return base + NS * (T::A + T::W) + s * T::S; };
+  auto slot_r = [&](uint32_t i) { return base + NS * (T::A + T::W + T::S) + (i & 1) * T::R; };
   const uint32_t lds0 = lds_address(lds);
 
   // ---- copies: unit `wave * I + i` of 64 of the step's, one 16-byte unit (scales: one byte) a lane.
@@ -191,43 +202,46 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
   }
   const int64_t step_w = kBack ? 64 * (int64_t)half : 32, step_s = kBack ? 64 * (int64_t)blocks : 2;
   auto inside = [&](uint32_t t, int at) {  // row or block `at` of step t lies before the end of the sum
-    return kBack ? 64 * t + at < sum : 2 * t + at < blocks;
+    return 64 * t + (kBack ? 1 : 32) * at < end;
   };
-  // the weights and scales of step t to ring slot s; WHOLE: all of it lies before
-  // the end of the sum
-  auto copy_weights = [&](uint32_t t, uint32_t s, auto WHOLE) {
+  // the weights and scales of the group's step i to ring slot s; WHOLE: all of it
+  // lies before the end of the sum
+  auto copy_weights = [&](uint32_t i, uint32_t s, auto WHOLE) {
     constexpr bool whole = decltype(WHOLE)::value;
+    const uint32_t t = step_at(i);
 #pragma unroll
-    for (int i = 0; i < T::IW; ++i) {
-      const uint8_t* from = wp[i] + t * step_w;
-      if (!whole) from = inside(t, at_w(lane, i)) ? from : zeros;
-      copy16(from, lds0 + 16 * (slot_w(s) + (wave * T::IW + i) * 64));
+    for (int c = 0; c < T::IW; ++c) {
+      const uint8_t* from = wp[c] + t * step_w;
+      if (!whole) from = inside(t, at_w(lane, c)) ? from : zeros;
+      copy16(from, lds0 + 16 * (slot_w(s) + (wave * T::IW + c) * 64));
     }
 #pragma unroll
-    for (int i = 0; i < T::IS; ++i) {
-      const uint8_t* from = sp[i] + t * step_s;
-      if (!whole) from = inside(t, at_s(lane, i)) ? from : zeros;
-      copy_byte(from, lds0 + 16 * slot_s(s) + (wave * T::IS + i) * 256);
+    for (int c = 0; c < T::IS; ++c) {
+      const uint8_t* from = sp[c] + t * step_s;
+      if (!whole) from = inside(t, at_s(lane, c)) ? from : zeros;
+      copy_byte(from, lds0 + 16 * slot_s(s) + (wave * T::IS + c) * 256);
     }
   };
-  // step t to ring slot s (backward: with the weights of step t + 1, to the next slot)
-  auto copy = [&](uint32_t t, uint32_t s, auto WHOLE) {
+  // step i to ring slot s (backward: with the weights of step i + 1, to the next slot)
+  auto copy = [&](uint32_t i, uint32_t s, auto WHOLE) {
+    const uint32_t t = step_at(i);
     const uint32_t to_a = lds0 + 16 * (slot_a(s) + wave * T::IA * 64);
     const uint8_t* const xs = uniform(xb + (uint64_t)t * 128);
 #pragma unroll
-    for (int i = 0; i < T::IA; ++i) {
+    for (int c = 0; c < T::IA; ++c) {
       if constexpr (decltype(WHOLE)::value)
-        copy16(xs, xv[i], to_a + i * 1024);
+        copy16(xs, xv[c], to_a + c * 1024);
       else
-        copy16(64 * t + 8 * unit_x(lane, i) < sum ? xs + xv[i] : zeros, to_a + i * 1024);
+        copy16(64 * t + 8 * unit_x(lane, c) < end ? xs + xv[c] : zeros, to_a + c * 1024);
     }
     if constexpr (kBack)
-      copy_weights(t + 1, s + 1 == NS ? 0 : s + 1, WHOLE);
+      copy_weights(i + 1, s + 1 == NS ? 0 : s + 1, WHOLE);
     else
-      copy_weights(t, s, WHOLE);
+      copy_weights(i, s, WHOLE);
   };
-  // steps t that copy() may take as whole
-  const uint32_t whole = kBack ? (sum >= 64 ? sum / 64 - 1 : 0) : sum / 64;
+  // steps i that copy() may take as whole
+  const uint32_t full = end / 64 > step_at(0) ? (end / 64 - step_at(0) + T::WK - 1) / T::WK : 0;
+  const uint32_t whole = kBack && full > 0 ? full - 1 : full;
 
   f32x16 acc[MT][2];
 #pragma unroll
@@ -276,8 +290,8 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 2)),
                    __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 3))};
   };
-  // a quarter's weights of step t: forward rebuilt, backward read as they were rebuilt
-  auto weights = [&](Weights& v, const Step& st, uint32_t t, auto Q) {
+  // a quarter's weights of step n: forward rebuilt, backward read as they were rebuilt
+  auto weights = [&](Weights& v, const Step& st, uint32_t n, auto Q) {
     constexpr int q = decltype(Q)::value;
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -287,7 +301,7 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
 #pragma unroll
         for (int d = 0; d < 2; ++d) {
           const int row = 32 * h + 8 * q + 4 * d + (p >> 2);
-          const u32x4* const at = lds + slot_r(t) + row * (T::BN / 8) + swizzle_r<T::BN>(row, c >> 3);
+          const u32x4* const at = lds + slot_r(n) + row * (T::BN / 8) + swizzle_r<T::BN>(row, c >> 3);
           const u32x2 x = __builtin_bit_cast(
               u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(
                          (__attribute__((address_space(3))) i16x4*)(reinterpret_cast<const u32x2*>(at) + (p & 1))));
@@ -299,7 +313,7 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
       }
     }
   };
-  // ---- backward: the weights of step t, in ring slot s, rebuilt to rows of bf16.
+  // ---- backward: the weights of step n, in ring slot s, rebuilt to rows of bf16.
   // A wave takes the units that it copied itself: 32 values of one row and block.
   struct Unit {
     u32x4 w;
@@ -310,11 +324,11 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
     v.w = lds[slot_w(s) + u];
     v.s = reinterpret_cast<const uint32_t*>(lds + slot_s(s))[u];
   };
-  auto rebuild_unit = [&](const Unit& v, uint32_t t, int i) {
+  auto rebuild_unit = [&](const Unit& v, uint32_t n, int i) {
     const int u = (wave * T::IW + i) * 64 + lane, row = u / U, c = u % U;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      lds[slot_r(t) + row * (T::BN / 8) + swizzle_r<T::BN>(row, 4 * c + e)] = rebuild8(v.w[e], v.s);
+      lds[slot_r(n) + row * (T::BN / 8) + swizzle_r<T::BN>(row, 4 * c + e)] = rebuild8(v.w[e], v.s);
   };
   auto multiply_row = [&](const Quarter& o, const Weights& v, int i) {
 #pragma unroll
@@ -354,90 +368,124 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
   Quarter o0, o1;
   Weights b0, b1;
   Unit unit;
-  uint32_t cur = t0 % NS;
-  auto step = [&](uint32_t t, auto FAST) {
-    constexpr bool fast = decltype(FAST)::value;  // step t + NS exists and is whole
+  uint32_t cur = 0;
+  auto step = [&](uint32_t n, auto FAST) {
+    constexpr bool fast = decltype(FAST)::value;  // step n + NS exists and is whole
     const uint32_t next = cur + 1 == NS ? 0 : cur + 1;
     if constexpr (kBack) read_unit(unit, next, 0);
     read(o1, cur, Q1{});
-    weights(b1, st, t, Q1{});
+    weights(b1, st, n, Q1{});
     multiply(o0, b0);
     interleave();
     if constexpr (kBack) {
-      rebuild_unit(unit, t + 1, 0);
+      rebuild_unit(unit, n + 1, 0);
       if constexpr (T::IW > 1) read_unit(unit, next, 1);
     }
     read(o0, cur, Q2{});
-    weights(b0, st, t, Q2{});
+    weights(b0, st, n, Q2{});
     multiply(o1, b1);
     interleave();
-    if constexpr (kBack && T::IW > 1) rebuild_unit(unit, t + 1, 1);
+    if constexpr (kBack && T::IW > 1) rebuild_unit(unit, n + 1, 1);
     read(o1, cur, Q3{});
-    weights(b1, st, t, Q3{});
+    weights(b1, st, n, Q3{});
     multiply(o0, b0);
     interleave();
     // the last operands (on every path here: after the branch the compiler's
     // own wait would be for the next step's reads too)
     __builtin_amdgcn_s_waitcnt(kWaitLds);
-    if (fast || t + 1 < t1) {
+    if (fast || n + 1 < count) {
       // the next step's copies: all but those of the NS - 2 steps after it
-      if (fast || t + NS <= t1)
+      if (fast || n + NS <= count)
         __builtin_amdgcn_s_waitcnt(wait_vm((NS - 2) * T::COPIES));
       else
         __builtin_amdgcn_s_waitcnt(wait_vm(0));
       lds_barrier();
       read_step(st, next);
       read(o0, next, Q0{});
-      if constexpr (kBack) weights(b0, st, t + 1, Q0{});
+      if constexpr (kBack) weights(b0, st, n + 1, Q0{});
       __builtin_amdgcn_sched_barrier(0);
       if constexpr (!fast) {
-        if (t + NS < t1) copy(t + NS, cur, std::false_type{});
+        if (n + NS < count) copy(n + NS, cur, std::false_type{});
         __builtin_amdgcn_sched_barrier(0);
       }
     }
     multiply_row(o1, b1, 0);
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (fast) copy(t + NS, cur, std::true_type{});
+    if constexpr (fast) copy(n + NS, cur, std::true_type{});
     __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int i = 1; i < MT; ++i) multiply_row(o1, b1, i);
     __builtin_amdgcn_sched_barrier(0);
-    if constexpr (!kBack) weights(b0, st, t + 1, Q0{});  // (of no step, behind the last)
+    if constexpr (!kBack) weights(b0, st, n + 1, Q0{});  // (of no step, behind the last)
     cur = next;
   };
-  if constexpr (kBack) copy_weights(t0, cur, std::false_type{});
+  if constexpr (kBack) copy_weights(0, 0, std::false_type{});
 #pragma unroll
   for (int i = 0; i < NS; ++i) {
     if (kBack && i == NS - 1) {
       // these copies bring weights to the slot of t0's, which are rebuilt first
       // (behind a barrier: nothing else keeps their reads below the wait)
-      if (t0 + NS - 1 <= t1)
+      if (NS - 1 <= count)
         __builtin_amdgcn_s_waitcnt(wait_vm((NS - 1) * T::COPIES));
       else
         __builtin_amdgcn_s_waitcnt(wait_vm(0));
       lds_barrier();
 #pragma unroll
       for (int j = 0; j < T::IW; ++j) {
-        read_unit(unit, cur, j);
-        rebuild_unit(unit, t0, j);
+        read_unit(unit, 0, j);
+        rebuild_unit(unit, 0, j);
       }
       __builtin_amdgcn_s_waitcnt(kWaitLds);
       lds_barrier();
     }
-    if (t0 + i < t1) copy(t0 + i, (t0 + i) % NS, std::false_type{});
+    if (i < count) copy(i, i, std::false_type{});
   }
-  if (t0 + NS <= t1)
+  if (NS <= count)
     __builtin_amdgcn_s_waitcnt(wait_vm((NS - 1) * T::COPIES));
   else
     __builtin_amdgcn_s_waitcnt(wait_vm(0));
   lds_barrier();
-  read_step(st, cur);
-  read(o0, cur, Q0{});
-  weights(b0, st, t0, Q0{});
-  const uint32_t tw = whole < t1 ? whole : t1;  // steps t with t + NS < tw are fast
-  uint32_t t = t0;
-  for (; t + NS < tw; ++t) step(t, std::true_type{});
-  for (; t < t1; ++t) step(t, std::false_type{});
+  read_step(st, 0);
+  read(o0, 0, Q0{});
+  weights(b0, st, 0, Q0{});
+  const uint32_t fast = whole < count ? whole : count;  // steps n with n + NS < fast
+  uint32_t n = 0;
+  for (; n + NS < fast; ++n) step(n, std::true_type{});
+  for (; n < count; ++n) step(n, std::false_type{});
+
+  // ---- the groups' sums, in the order of the groups, to the first one, which goes
+  // on (the others keep it company at the barriers)
+  if constexpr (T::WK > 1) {
+    constexpr int kVectors = MT * 2 * 4;  // of a thread
+    f32x4* const sums = reinterpret_cast<f32x4*>(lds) + wave * 64 + lane;
+    __syncthreads();  // (every copy has arrived and every operand is read)
+    if (group > 0) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+          for (int v = 0; v < 4; ++v)
+            sums[((group - 1) * kVectors + (i * 2 + j) * 4 + v) * (64 * T::NW)] =
+                (f32x4){acc[i][j][4 * v], acc[i][j][4 * v + 1], acc[i][j][4 * v + 2], acc[i][j][4 * v + 3]};
+    }
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll
+      for (int g = 1; g < T::WK; ++g)
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int v = 0; v < 4; ++v) {
+              const f32x4 x = sums[((g - 1) * kVectors + (i * 2 + j) * 4 + v) * (64 * T::NW)];
+#pragma unroll
+              for (int e = 0; e < 4; ++e) acc[i][j][4 * v + e] += x[e];
+            }
+    }
+  }
+  const bool lead = T::WK == 1 || group == 0;
 
   // ---- a part's sums: written, and by the last one of the tile's parts added in
   // order (the same bits whichever is last).  They are written and read with
@@ -445,19 +493,21 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
   // for its stores is all that the count needs before it: a release of the device
   // would write back an XCD's whole cache (13 against 9 us on a call of one row).
   if (splits > 1) {
-    constexpr int kPairs = MT * 2 * 8;  // of a thread
-    uint64_t* const parts = G.partial + (uint64_t)(tile - G.whole) * splits * (kPairs * T::THREADS) + tid;
-    uint64_t* const mine = parts + (uint64_t)split * (kPairs * T::THREADS);
+    constexpr int kPairs = MT * 2 * 8, kLead = 64 * T::NW;  // of a thread, threads
+    uint64_t* const parts = G.partial + (uint64_t)(tile - G.whole) * splits * (kPairs * kLead) + tid;
+    uint64_t* const mine = parts + (uint64_t)split * (kPairs * kLead);
+    if (lead) {
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+      for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
+        for (int j = 0; j < 2; ++j)
 #pragma unroll
-        for (int v = 0; v < 8; ++v) {
+          for (int v = 0; v < 8; ++v) {
           const f32x2 x = {acc[i][j][2 * v], acc[i][j][2 * v + 1]};
-          __hip_atomic_store(mine + ((i * 2 + j) * 8 + v) * T::THREADS, __builtin_bit_cast(uint64_t, x), __ATOMIC_RELAXED,
+          __hip_atomic_store(mine + ((i * 2 + j) * 8 + v) * kLead, __builtin_bit_cast(uint64_t, x), __ATOMIC_RELAXED,
                              __HIP_MEMORY_SCOPE_AGENT);
-        }
+          }
+    }
     asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
     __shared__ uint32_t before;
     __syncthreads();
@@ -467,7 +517,7 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
       if (before + 1 == splits) __hip_atomic_store(c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
     }
     __syncthreads();
-    if (before + 1 != splits) return;
+    if (before + 1 != splits || !lead) return;
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -480,7 +530,7 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
             if (p0 + p < splits) {
 #pragma unroll
               for (int v = 0; v < 8; ++v)
-                x[p][v] = __hip_atomic_load(parts + (uint64_t)(p0 + p) * (kPairs * T::THREADS) + ((i * 2 + j) * 8 + v) * T::THREADS,
+                x[p][v] = __hip_atomic_load(parts + (uint64_t)(p0 + p) * (kPairs * kLead) + ((i * 2 + j) * 8 + v) * kLead,
                                             __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
             }
 #pragma unroll
@@ -501,6 +551,8 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
         }
       }
   }
+
+  if (!lead) return;
 
   // ---- outputs.  D[row of x][column]: lane half h, register q hold row
   // 8 (q / 4) + 4 h + q % 4 of column r.  Stores go through a resource that ends
@@ -699,7 +751,7 @@ Plan make_plan(const MxBf16Problem& p) {
 
 template <int KIND, typename T>
 hipError_t launch_tile(const MxBf16Problem& p, const GemmArgs& g, uint32_t blocks, hipStream_t stream) {
-  constexpr int lds = 16 * (KIND == kMxBackward ? T::BACKWARD : T::FORWARD);
+  constexpr int lds = 16 * T::WK * (KIND == kMxBackward ? T::BACKWARD : T::FORWARD);
   // the LDS limit is raised once per device (one bit each for the first 64);
   // callers racing here all set the same value
   static std::atomic<uint64_t> configured{0};
