@@ -172,8 +172,12 @@ struct MxBf16Fill {
   virtual hipError_t operator()(MxBf16Problem& p, char* reserved) = 0;
 };
 hipError_t launch_mx_bf16_with(const MxBf16Problem& p, size_t reserve, MxBf16Fill* fill, hipStream_t stream);
+// at most 16 rows, forward (w4_mx_bf16_skinny.hip)
+int mx_bf16_skinny_shape(const MxBf16Problem& p);
+hipError_t launch_mx_bf16_skinny(const MxBf16Problem& p, int shape, hipStream_t stream);
 // For the tests, which name the kernel that they run: 16 * parts of the sum + tile
-// (w4_mx_bf16_gemm.hip), 1024 more where only the last tiles are cut into parts.  The kernel that a product takes:
+// (w4_mx_bf16_gemm.hip), 1024 more where only the last tiles are cut into parts, or
+// 4096 + shape (w4_mx_bf16_skinny.hip).  The kernel that a product takes:
 extern "C" int32_t w4_mx_bf16_kernel_of(int32_t kind, int64_t n, int64_t k, int64_t m);
 // The product (kind, sizes and pointers as in MxBf16Problem, x without padding)
 // on a kernel of the caller's choice; a hipError_t, an error where it does not fit.

@@ -281,15 +281,6 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
       v.a[i] = lds[slot_a(s) + 8 * row + ((4 * h + q) ^ swizzle_x(row))];
     }
   };
-  // Eight values of a dword at a scale byte: the conversion takes the exponent
-  // field of its scale and no other bit (0 stands for 2^-127 there, 255 gives NaN).
-  auto rebuild8 = [](uint32_t d, uint32_t scale) {
-    const float s = __builtin_bit_cast(float, scale << 23);
-    return (u32x4){__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 0)),
-                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 1)),
-                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 2)),
-                   __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 3))};
-  };
   // a quarter's weights of step n: forward rebuilt, backward read as they were rebuilt
   auto weights = [&](Weights& v, const Step& st, uint32_t n, auto Q) {
     constexpr int q = decltype(Q)::value;
@@ -309,7 +300,7 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
           v.b[j][2 * d + 1] = x.y;
         }
       } else {
-        v.b[j] = rebuild8(st.w[j][q], st.s[j]);
+        v.b[j] = mx_rebuild8(st.w[j][q], st.s[j]);
       }
     }
   };
@@ -328,7 +319,7 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
     const int u = (wave * T::IW + i) * 64 + lane, row = u / U, c = u % U;
 #pragma unroll
     for (int e = 0; e < 4; ++e)
-      lds[slot_r(n) + row * (T::BN / 8) + swizzle_r<T::BN>(row, 4 * c + e)] = rebuild8(v.w[e], v.s);
+      lds[slot_r(n) + row * (T::BN / 8) + swizzle_r<T::BN>(row, 4 * c + e)] = mx_rebuild8(v.w[e], v.s);
   };
   auto multiply_row = [&](const Quarter& o, const Weights& v, int i) {
 #pragma unroll
@@ -790,6 +781,9 @@ hipError_t launch_plan(const MxBf16Problem& problem, const Plan& q, size_t reser
   });
 }
 
+// Forward products with few rows have a kernel of their own.
+bool skinny(const MxBf16Problem& p) { return p.m <= 16 && p.kind != kMxBackward; }
+
 }  // namespace
 
 bool mx_bf16_fits(const MxBf16Problem& p) {
@@ -801,6 +795,7 @@ bool mx_bf16_fits(const MxBf16Problem& p) {
 }
 
 hipError_t launch_mx_bf16_with(const MxBf16Problem& p, size_t reserve, MxBf16Fill* fill, hipStream_t stream) {
+  if (skinny(p)) return launch_mx_bf16_skinny(p, mx_bf16_skinny_shape(p), stream);
   return launch_plan(p, make_plan(p), reserve, stream, [&](MxBf16Problem& on, char* ws) {
     return fill ? (*fill)(on, ws) : hipSuccess;
   });
@@ -808,6 +803,7 @@ hipError_t launch_mx_bf16_with(const MxBf16Problem& p, size_t reserve, MxBf16Fil
 
 extern "C" int32_t w4_mx_bf16_kernel_of(int32_t kind, int64_t n, int64_t k, int64_t m) {
   const MxBf16Problem p{nullptr, nullptr, nullptr, nullptr, nullptr, m, n, k, kind == kMxBackward ? n : k, 0, 0, kind};
+  if (skinny(p)) return 4096 + mx_bf16_skinny_shape(p);
   const Plan q = make_plan(p);
   return (q.whole > 0 && q.splits > 1 ? 1024 : 0) + 16 * (int32_t)q.splits + q.tile;
 }
@@ -817,6 +813,10 @@ extern "C" int32_t w4_mx_bf16_product_on(int32_t kernel, int32_t kind, int32_t a
                                          uint16_t* gu, void* y, int32_t y_bf16, void* stream) {
   const MxBf16Problem p{w, w_scales, x, y, gu, m, n, k, kind == kMxBackward ? n : k, y_bf16, act, kind};
   if (kind < kMxForward || kind > kMxBackward || (kind == kMxBackward && n % 8)) return hipErrorInvalidValue;
+  if (kernel >= 4096) {
+    if (kernel > 4098 || kind == kMxBackward || m > 16) return hipErrorInvalidValue;
+    return launch_mx_bf16_skinny(p, kernel - 4096, static_cast<hipStream_t>(stream));
+  }
   const int32_t parts = kernel % 1024 / 16, tile = kernel % 16;
   if (kernel < 0 || kernel >= 2048 || tile >= kTiles || parts < 1 || parts > (int32_t)kMaxSplits)
     return hipErrorInvalidValue;

@@ -239,6 +239,18 @@ __device__ __forceinline__ void mx_store4(void* y, int y_bf16, int64_t row_base,
   }
 }
 
+// Eight values of a dword of fp4 elements as bf16, at the scale byte in the low bits
+// of a dword: exact but for values below 2^-126, which bf16 rounds to nearest even.
+// The conversion takes the exponent field of its scale operand and no other bit (the
+// dword's other bytes may be anything); 0 stands for 2^-127 there, 255 gives NaN.
+__device__ __forceinline__ u32x4 mx_rebuild8(uint32_t d, uint32_t scale) {
+  const float s = __builtin_bit_cast(float, scale << 23);
+  return (u32x4){__builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 0)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 1)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 2)),
+                 __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(d, s, 3))};
+}
+
 // D[16][16] += A[16][128] B[128][16] with block scales.  Lane l: row (A) or
 // column (B) l % 16; with g = l / 16, fp4 registers 0-3 hold k = 32 g .. + 31,
 // fp8 registers 0-3 k = 16 g .. + 15 and registers 4-7 k = 64 + 16 g .. + 15;
