@@ -27,6 +27,7 @@
 #include "w4_lds_copy.h"
 #include "w4_mx_act.h"
 #include "w4_mx_device.h"
+#include "w4_mx_parts.h"
 
 namespace w4 {
 namespace {
@@ -55,9 +56,9 @@ struct Tile {
 };
 using T0 = Tile<256, 256, 2, 4, 1, 3, 2>;
 using T1 = Tile<128, 256, 2, 4, 1, 3, 3>;
-using T2 = Tile<128, 128, 2, 2, 2, 3, 2>;
+using T2 = Tile<128, 128, 2, 2, 1, 3, 2>;
 using T3 = Tile<64, 128, 2, 2, 2, 3, 2>;
-using T4 = Tile<32, 64, 1, 1, 4, 3, 2>;
+using T4 = Tile<32, 64, 1, 1, 4, 3, 2>;  // (backward: the narrow kernel, whose tiles are the same)
 constexpr int kTiles = 5;
 
 constexpr uint32_t kMaxSplits = 16;
@@ -478,69 +479,23 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
   }
   const bool lead = T::WK == 1 || group == 0;
 
-  // ---- a part's sums: written, and by the last one of the tile's parts added in
-  // order (the same bits whichever is last).  They are written and read with
-  // device scope, past the caches that belong to one XCD, so that a wave's wait
-  // for its stores is all that the count needs before it: a release of the device
-  // would write back an XCD's whole cache (13 against 9 us on a call of one row).
   if (splits > 1) {
     constexpr int kPairs = MT * 2 * 8, kLead = 64 * T::NW;  // of a thread, threads
     uint64_t* const parts = G.partial + (uint64_t)(tile - G.whole) * splits * (kPairs * kLead) + tid;
-    uint64_t* const mine = parts + (uint64_t)split * (kPairs * kLead);
-    if (lead) {
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < 2; ++j)
-#pragma unroll
-          for (int v = 0; v < 8; ++v) {
-          const f32x2 x = {acc[i][j][2 * v], acc[i][j][2 * v + 1]};
-          __hip_atomic_store(mine + ((i * 2 + j) * 8 + v) * kLead, __builtin_bit_cast(uint64_t, x), __ATOMIC_RELAXED,
-                             __HIP_MEMORY_SCOPE_AGENT);
-          }
-    }
-    asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-    __shared__ uint32_t before;
-    __syncthreads();
-    if (tid == 0) {
-      uint32_t* const c = G.counted + (tile - G.whole);
-      before = __hip_atomic_fetch_add(c, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-      if (before + 1 == splits) __hip_atomic_store(c, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    }
-    __syncthreads();
-    if (before + 1 != splits || !lead) return;
+    if (lead)
+      put_part<kPairs>(parts + (uint64_t)split * (kPairs * kLead), kLead, [&](int v) {
+        const f32x16& a = acc[v / 16][v / 8 % 2];
+        return (f32x2){a[v % 8 * 2], a[v % 8 * 2 + 1]};
+      });
+    if (!last_part(G.counted + (tile - G.whole), splits) || !lead) return;
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int j = 0; j < 2; ++j) {
-        f32x2 total[8];
-        for (uint32_t p0 = 0; p0 < splits; p0 += 4) {  // (eight pairs of four parts in flight)
-          uint64_t x[4][8];
-#pragma unroll
-          for (uint32_t p = 0; p < 4; ++p)
-            if (p0 + p < splits) {
-#pragma unroll
-              for (int v = 0; v < 8; ++v)
-                x[p][v] = __hip_atomic_load(parts + (uint64_t)(p0 + p) * (kPairs * kLead) + ((i * 2 + j) * 8 + v) * kLead,
-                                            __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            }
-#pragma unroll
-          for (uint32_t p = 0; p < 4; ++p)
-            if (p0 + p < splits) {
-#pragma unroll
-              for (int v = 0; v < 8; ++v) {
-                const f32x2 y = __builtin_bit_cast(f32x2, x[p][v]);
-                total[v].x = p0 + p == 0 ? y.x : total[v].x + y.x;
-                total[v].y = p0 + p == 0 ? y.y : total[v].y + y.y;
-              }
-            }
-        }
-#pragma unroll
-        for (int v = 0; v < 8; ++v) {
-          acc[i][j][2 * v] = total[v].x;
-          acc[i][j][2 * v + 1] = total[v].y;
-        }
-      }
+      for (int j = 0; j < 2; ++j)
+        add_parts<8, 4>(parts + (i * 2 + j) * 8 * kLead, kPairs * kLead, kLead, splits, [&](int v, const f32x2& x) {
+          acc[i][j][2 * v] = x.x;
+          acc[i][j][2 * v + 1] = x.y;
+        });
   }
 
   if (!lead) return;
@@ -702,34 +657,62 @@ Plan plan_on(const MxBf16Problem& p, int t, uint32_t s, int64_t whole) {
   constexpr int64_t kTileBytes = (INT64_C(1) << 31) - 1;
   if (4 * wide > kTileBytes / T::BM || 2 * p.x_pitch > kTileBytes / T::BM) q.tile = -1;
   if (q.whole > tiles || (int64_t)s > steps_of(p) || (s > 1 && q.cut() > kMaxCut)) q.tile = -1;
+  if (std::is_same_v<T, T4> && p.kind == kMxBackward && s > 1 && q.whole > 0) q.tile = -1;  // (all tiles or none)
   if ((tiles * s + 14) * T::THREADS > kMaxLaunchThreads) q.tile = -1;
   return q;
 }
 
-// What a tile costs: first + step us for its start and end and per 64 of the
-// sum, by the blocks that share a CU.
+// What a product costs on a tile: a block alone on its CU takes first + step us for
+// its start and end and per step of a group, two blocks that share one (where they
+// fit) first2 + step2; a launch takes `launch`, and sums in parts take `join` and, for
+// each part, `part` and its bytes at 64 KB a `copy`.  Fitted to 4200 times of every
+// tile and number of parts over 17 to 1500 rows, 300 to 22016 columns and sums of 300
+// to 22016 (root mean square of the error 8 to 10%); the plans they choose take 1.3%
+// more than the best ones on average.  Examples (us, graph replays): 64 x 1000 x 4096
+// 8.5 on tile 4 in four parts, 1 part 12.3, tile 3 in eight parts 12; gated 333 x 2730 x
+// 2080 20.6 on tile 2, 23.4 on tile 3, 24.2 on tile 4; backward 2048 x 4096 x 11008 171
+// on tile 0 with the last round's tiles in two parts, 192 without.
 struct Cost {
-  float first, step;
-  int per_cu;
+  float first, step, first2, step2;  // first2 == 0: one block a CU
 };
-constexpr Cost kCost[kTiles] = {{7.0f, 1.55f, 1}, {4.0f, 0.90f, 1}, {3.0f, 0.55f, 1}, {2.5f, 0.40f, 1}, {2.0f, 0.35f, 1}};
+struct Costs {
+  Cost tile[kTiles];
+  float launch, join, part, copy;
+};
+constexpr Costs kCosts[3] = {
+    {{{7.85f, 1.03f, 0, 0}, {3.90f, 0.69f, 0, 0}, {2.12f, 0.42f, 7.23f, 0.80f}, {0.89f, 0.64f, 3.23f, 1.23f}, {1.76f, 0.42f, 2.33f, 0.77f}},
+     1.8f, 1.95f, 0.28f, 0.9f},
+    {{{13.0f, 1.08f, 0, 0}, {6.29f, 0.71f, 0, 0}, {3.35f, 0.42f, 7.62f, 0.83f}, {1.12f, 0.66f, 3.60f, 1.23f}, {1.83f, 0.42f, 3.07f, 0.79f}},
+     2.6f, 1.97f, 0.28f, 0.9f},
+    {{{8.43f, 1.32f, 0, 0}, {5.08f, 0.94f, 0, 0}, {3.64f, 0.62f, 9.17f, 0.92f}, {3.40f, 0.80f, 0, 0}, {2.14f, 0.78f, 2.78f, 1.37f}},
+     0.6f, 2.23f, 0.11f, 1.0f}};
 
 Plan make_plan(const MxBf16Problem& p) {
   const int64_t cus = device_cus();
+  const Costs& costs = kCosts[p.kind];
   Plan best{4, 1, 0, 0, 0};
   double least = 0;
   for (int t = 0; t < kTiles; ++t)
     with_tile(t, [&](auto X) {
+      using T = decltype(X);
+      const Cost& c = costs.tile[t];
+      // blocks of so many steps each, in rounds over the CUs
+      auto rounds = [&](int64_t blocks, int64_t steps) {
+        const double alone = c.first + c.step * (double)((steps + T::WK - 1) / T::WK);
+        if (c.first2 == 0) return (double)((blocks + cus - 1) / cus) * alone;
+        const double pair = c.first2 + c.step2 * (double)((steps + T::WK - 1) / T::WK);
+        const int64_t rest = blocks % (2 * cus);
+        return (double)(blocks / (2 * cus)) * pair + (rest > cus ? pair : rest > 0 ? alone : 0);
+      };
       for (uint32_t s : {1u, 2u, 3u, 4u, 6u, 8u, 12u, 16u}) {
-        Plan q = plan_on<decltype(X)>(p, t, s, 0);
+        Plan q = plan_on<T>(p, t, s, 0);
         const int64_t tiles = q.tiles_m * q.tiles_n;
-        if (s > 1 && tiles > cus) q = plan_on<decltype(X)>(p, t, s, tiles / cus * cus);
+        if (s > 1 && tiles > cus) q = plan_on<T>(p, t, s, tiles / cus * cus);
         if (q.tile < 0) continue;
-        const double k = (double)steps_of(p), part = (double)((steps_of(p) + s - 1) / s);
-        double us = (double)((q.whole + cus - 1) / cus) * (kCost[t].first + kCost[t].step * k);
+        double us = costs.launch + rounds(q.whole, steps_of(p));
         if (s > 1)
-          us += (double)((q.cut() * s + cus - 1) / cus) * (kCost[t].first + kCost[t].step * part) + 3.0 +
-                s * decltype(X)::BM * decltype(X)::BN * 4 / 50000.0;
+          us += rounds(q.cut() * s, (steps_of(p) + s - 1) / s) + costs.join +
+                s * (costs.part + costs.copy * T::BM * T::BN / 16384.0);
         if (best.tiles_m == 0 || us < least) {
           least = us;
           best = q;
@@ -776,8 +759,11 @@ hipError_t launch_plan(const MxBf16Problem& problem, const Plan& q, size_t reser
     g.partial = reinterpret_cast<uint64_t*>(ws + reserve);
     const uint32_t blocks = (uint32_t)q.blocks();
     if (p.kind == kMxGated) return launch_tile<kMxGated, T>(p, g, blocks, stream);
-    if (p.kind == kMxBackward) return launch_tile<kMxBackward, T>(p, g, blocks, stream);
-    return launch_tile<kMxForward, T>(p, g, blocks, stream);
+    if (p.kind == kMxForward) return launch_tile<kMxForward, T>(p, g, blocks, stream);
+    if constexpr (std::is_same_v<T, T4>)
+      return launch_mx_bf16_narrow(p, q.splits, ws + reserve, g.counted, stream);
+    else
+      return launch_tile<kMxBackward, T>(p, g, blocks, stream);
   });
 }
 
