@@ -11,25 +11,29 @@ namespace w4 {
 // Codes, as w4_activation.
 constexpr int kSilu = 0, kGelu = 1, kGeluTanh = 2;
 
-// p = 1 / (1 + e^-z) and q = 1 - p = 1 / (1 + e^z), each to a few 2^-24 of itself
-// wherever it is a normal number: both come from e = e^-|z| <= 1, so neither
-// cancels nor overflows.  e = 2^t with t = -|z| log2(e) kept as two floats (the
-// rounding of t alone would cost |t| 2^-24 of the result).  Beyond |z| = 128, e
-// is below the smallest normal number and taken as at 128.  A NaN's value is
-// any: every caller multiplies by what made it.
-__device__ __forceinline__ void sigmoid_pair(float z, float& p, float& q) {
-  const float a = -fminf(fabsf(z), 128.0f);
+// e^a, a <= 0, to a few 2^-24 of itself: 2^t with t = a log2(e) kept as two floats (the
+// rounding of t alone would cost |t| 2^-24 of the result); below 2^-126, 0.
+__device__ __forceinline__ float exp_down(float a) {
   constexpr float kL = 1.44269504e+00f, kLlo = 1.92596303e-08f;  // log2(e), and what its rounding leaves
   const float t = a * kL;
   const float lo = __builtin_fmaf(a, kLlo, __builtin_fmaf(a, kL, -t));
-  const float e0 = __builtin_amdgcn_exp2f(t);
-  const float e = __builtin_fmaf(e0, lo * 6.93147182e-01f, e0);  // 2^lo = 1 + lo ln 2, lo < 2^-16
-  const float d = 1.0f + e;
-  float r = __builtin_amdgcn_rcpf(d);
-  r = __builtin_fmaf(__builtin_fmaf(-d, r, 1.0f), r, r);
-  const bool up = z >= 0.0f;
-  p = up ? r : e * r;
-  q = up ? e * r : r;
+  const float e = __builtin_amdgcn_exp2f(t);
+  return __builtin_fmaf(e, lo * 6.93147182e-01f, e);  // 2^lo = 1 + lo ln 2, lo < 2^-16
+}
+
+// 1 / (1 + e^-z), to a few 2^-24 of itself wherever it is a normal number: e^-|z| <= 1
+// neither cancels nor overflows.  Beyond |z| = 128 it is taken as at 128, where
+// e^-|z| is 0.  A NaN's value is any: every caller multiplies by what made it.
+__device__ __forceinline__ float sigmoid(float z) {
+  const float e = exp_down(-fminf(fabsf(z), 128.0f));
+  return __builtin_amdgcn_rcpf(1.0f + e) * (z >= 0.0f ? 1.0f : e);
+}
+// It and 1 / (1 + e^z), which is 1 less it, without the cancellation.
+__device__ __forceinline__ void sigmoid_pair(float z, float& p, float& q) {
+  const float e = exp_down(-fminf(fabsf(z), 128.0f));
+  const float r = __builtin_amdgcn_rcpf(1.0f + e), s = e * r;
+  p = z >= 0.0f ? r : s;
+  q = z >= 0.0f ? s : r;
 }
 
 constexpr float kTanhA = 7.97884583e-01f;  // sqrt(2 / pi)
@@ -49,16 +53,9 @@ __device__ __forceinline__ float tanh_argument(float g) {  // 2y
 //   gelu_tanh  g (1 + tanh y) / 2 = g / (1 + e^-2y), y = sqrt(2/pi) (g + 0.044715 g^3)
 template <int ACT>
 __device__ __forceinline__ float activate(float g) {
-  float p, q;
-  if constexpr (ACT == kSilu) {
-    sigmoid_pair(g, p, q);
-    return g * p;
-  } else if constexpr (ACT == kGelu) {
-    return g * (0.5f * erfcf(g * -7.07106769e-01f));
-  } else {
-    sigmoid_pair(tanh_argument(g), p, q);
-    return g * p;
-  }
+  if constexpr (ACT == kSilu) return g * sigmoid(g);
+  if constexpr (ACT == kGelu) return g * (0.5f * erfcf(g * -7.07106769e-01f));
+  return g * sigmoid(tanh_argument(g));
 }
 
 // act(g) and act'(g) (a NaN where g is no number or infinite).

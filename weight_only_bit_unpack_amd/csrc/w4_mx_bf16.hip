@@ -2,8 +2,7 @@
 // backward pass up to its product, rows padded to whole 16-byte units, and the
 // workspace that holds them and the product's partial sums.
 //
-// Bound by HBM: each value is read or written once, eight a thread (16 bytes) where
-// the rows are whole units.
+// Bound by HBM: each value is read or written once, eight a thread.
 #include <type_traits>
 
 #include "w4_launch.h"
@@ -22,12 +21,13 @@ __device__ __forceinline__ void gate_grad(float dh, float g, float u, float& dg,
   du = dh * a;
 }
 
-// n and n / 8 units of a row; the threads take units in order.
+// Blocks of 256 threads take a row's values 2048 at a time (`chunks` of them a row),
+// eight a thread: as one unit of 16 bytes where the rows are whole units, ...
 template <int ACT>
-__global__ __launch_bounds__(256) void gate_grad_kernel(MxGateGrad G, int64_t first, int64_t count) {
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (at >= count) return;
-  const int64_t units = G.n >> 3, row = (first + at) / units, c = (first + at) - row * units;
+__global__ __launch_bounds__(256) void gate_grad_kernel(MxGateGrad G, uint32_t chunks, int64_t first) {
+  const int64_t at = first + blockIdx.x, row = at / chunks;
+  const int64_t units = G.n >> 3, c = (at - row * chunks) * 256 + threadIdx.x;
+  if (c >= units) return;
   const int64_t g0 = 2 * row * units + c;
   float dh[8], g[8], u[8];
   to_f32<kBf16>(load8<kBf16>(G.dh, row * units + c), dh);
@@ -39,43 +39,65 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(MxGateGrad G, int64_t fi
   store8<kBf16>(G.dgu, g0 + units, from_f32<kBf16>(u));
 }
 
-// The same for any n, a value of each half a thread; `padded` (or nullptr) gets
-// dgu with rows of `pitch` values, the ones behind the row's end zeros.
+// ... and otherwise 256 apart.  `padded` (or nullptr) gets dgu with rows of `pitch`
+// values, the ones behind the row's end zeros.
 template <int ACT>
-__global__ __launch_bounds__(256) void gate_grad_any_kernel(MxGateGrad G, int64_t first, int64_t count,
+__global__ __launch_bounds__(256) void gate_grad_any_kernel(MxGateGrad G, uint32_t chunks, int64_t first,
                                                             uint16_t* padded, int64_t pitch) {
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (at >= count) return;
-  const int64_t n = G.n, row = (first + at) / n, c = (first + at) - row * n;
-  const int64_t g0 = 2 * row * n + c;
-  float dg, du;
-  gate_grad<ACT>(bf16_bits_to_f32(G.dh[row * n + c]), bf16_bits_to_f32(G.gu[g0]), bf16_bits_to_f32(G.gu[g0 + n]), dg,
-                 du);
-  const uint16_t a = (uint16_t)f32_to_bf16_bits(dg), b = (uint16_t)f32_to_bf16_bits(du);
-  G.dgu[g0] = a;
-  G.dgu[g0 + n] = b;
-  if (padded) {
-    uint16_t* const p = padded + row * pitch;
-    p[c] = a;
-    p[n + c] = b;
-    if (c < pitch - 2 * n) p[2 * n + c] = 0;  // (at most 7)
+  const int64_t at = first + blockIdx.x, row = at / chunks, n = G.n;
+  const int64_t c0 = (at - row * chunks) * 2048 + threadIdx.x;
+  const uint16_t* const dh = G.dh + row * n;
+  const uint16_t* const gu = G.gu + 2 * row * n;
+  uint16_t* const dgu = G.dgu + 2 * row * n;
+  uint16_t* const pad = padded + row * pitch;
+  uint16_t x[8], g[8], u[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t c = c0 + 256 * i < n ? c0 + 256 * i : n - 1;
+    x[i] = dh[c];
+    g[i] = gu[c];
+    u[i] = gu[n + c];
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t c = c0 + 256 * i;
+    if (c >= n) continue;
+    float dg, du;
+    gate_grad<ACT>(bf16_bits_to_f32(x[i]), bf16_bits_to_f32(g[i]), bf16_bits_to_f32(u[i]), dg, du);
+    const uint16_t a = (uint16_t)f32_to_bf16_bits(dg), b = (uint16_t)f32_to_bf16_bits(du);
+    dgu[c] = a;
+    dgu[n + c] = b;
+    if (padded) {
+      pad[c] = a;
+      pad[n + c] = b;
+      if (c < pitch - 2 * n) pad[2 * n + c] = 0;  // (at most 7)
+    }
   }
 }
 
-// rows of n values to rows of `pitch`, zeros behind; a value a thread
+// rows of n values to rows of `pitch`, zeros behind
 __global__ __launch_bounds__(256) void pad_kernel(const uint16_t* x, int64_t n, uint16_t* y, int64_t pitch,
-                                                  int64_t first, int64_t count) {
-  const int64_t at = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  if (at >= count) return;
-  const int64_t row = (first + at) / pitch, c = (first + at) - row * pitch;
-  y[first + at] = c < n ? x[row * n + c] : (uint16_t)0;
+                                                  uint32_t chunks, int64_t first) {
+  const int64_t at = first + blockIdx.x, row = at / chunks;
+  const int64_t c0 = (at - row * chunks) * 2048 + threadIdx.x;
+  uint16_t v[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int64_t c = c0 + 256 * i;
+    v[i] = c < n ? x[row * n + c] : (uint16_t)0;
+  }
+#pragma unroll
+  for (int i = 0; i < 8; ++i)
+    if (c0 + 256 * i < pitch) y[row * pitch + c0 + 256 * i] = v[i];
 }
 
-// f(first, count, grid) over launches of at most 2^31 threads
+// f(chunks, first, grid) over launches of at most 2^23 blocks: rows of n values in
+// chunks of 2048
 template <typename F>
-hipError_t in_launches(int64_t total, F&& f) {
-  return in_parts(total, INT64_C(1) << 31, [&](int64_t first, int64_t count) {
-    f(first, count, dim3((uint32_t)((count + 255) / 256)));
+hipError_t over_rows(int64_t rows, int64_t n, F&& f) {
+  const int64_t chunks = (n + 2047) / 2048;
+  return in_parts(rows * chunks, INT64_C(1) << 23, [&](int64_t first, int64_t count) {
+    f((uint32_t)chunks, first, dim3((uint32_t)count));
     return hipGetLastError();
   });
 }
@@ -108,8 +130,8 @@ hipError_t launch_padded(const MxBf16Problem& p, hipStream_t stream, F&& write) 
 hipError_t launch_mx_bf16(const MxBf16Problem& p, hipStream_t stream) {
   if (p.kind != kMxBackward || p.n % 8 == 0) return launch_mx_bf16_with(p, 0, nullptr, stream);
   return launch_padded(p, stream, [&](uint16_t* rows, int64_t pitch) {
-    return in_launches(p.m * pitch, [&](int64_t first, int64_t count, dim3 grid) {
-      pad_kernel<<<grid, dim3(256), 0, stream>>>(p.x, p.n, rows, pitch, first, count);
+    return over_rows(p.m, pitch, [&](uint32_t chunks, int64_t first, dim3 grid) {
+      pad_kernel<<<grid, dim3(256), 0, stream>>>(p.x, p.n, rows, pitch, chunks, first);
     });
   });
 }
@@ -117,8 +139,8 @@ hipError_t launch_mx_bf16(const MxBf16Problem& p, hipStream_t stream) {
 hipError_t launch_mx_gated_grad(const MxGateGrad& g, const MxBf16Problem& p, hipStream_t stream) {
   auto any = [&](uint16_t* rows, int64_t pitch) {
     return with_activation(g.act, [&](auto ACT) {
-      return in_launches(g.m * g.n, [&](int64_t first, int64_t count, dim3 grid) {
-        gate_grad_any_kernel<decltype(ACT)::value><<<grid, dim3(256), 0, stream>>>(g, first, count, rows, pitch);
+      return over_rows(g.m, g.n, [&](uint32_t chunks, int64_t first, dim3 grid) {
+        gate_grad_any_kernel<decltype(ACT)::value><<<grid, dim3(256), 0, stream>>>(g, chunks, first, rows, pitch);
       });
     });
   };
@@ -126,8 +148,8 @@ hipError_t launch_mx_gated_grad(const MxGateGrad& g, const MxBf16Problem& p, hip
   hipError_t e;
   if (g.n % 8 == 0)
     e = with_activation(g.act, [&](auto ACT) {
-      return in_launches(g.m * (g.n / 8), [&](int64_t first, int64_t count, dim3 grid) {
-        gate_grad_kernel<decltype(ACT)::value><<<grid, dim3(256), 0, stream>>>(g, first, count);
+      return over_rows(g.m, g.n, [&](uint32_t chunks, int64_t first, dim3 grid) {
+        gate_grad_kernel<decltype(ACT)::value><<<grid, dim3(256), 0, stream>>>(g, chunks, first);
       });
     });
   else
