@@ -21,12 +21,12 @@ __device__ __forceinline__ void gate_grad(float dh, float g, float u, float& dg,
   du = dh * a;
 }
 
-// Blocks of 256 threads take a row's values 2048 at a time (`chunks` of them a row),
-// eight a thread: as one unit of 16 bytes where the rows are whole units, ...
+// Blocks of 256 threads take a row's values 2048 at a time (`chunks` blocks a row, from
+// row `first` on), eight a thread: as one unit of 16 bytes where the rows are whole units, ...
 template <int ACT>
 __global__ __launch_bounds__(256) void gate_grad_kernel(MxGateGrad G, uint32_t chunks, int64_t first) {
-  const int64_t at = first + blockIdx.x, row = at / chunks;
-  const int64_t units = G.n >> 3, c = (at - row * chunks) * 256 + threadIdx.x;
+  const int64_t row = first + blockIdx.x / chunks, units = G.n >> 3;
+  const int64_t c = (int64_t)(blockIdx.x % chunks) * 256 + threadIdx.x;
   if (c >= units) return;
   const int64_t g0 = 2 * row * units + c;
   float dh[8], g[8], u[8];
@@ -39,38 +39,45 @@ __global__ __launch_bounds__(256) void gate_grad_kernel(MxGateGrad G, uint32_t c
   store8<kBf16>(G.dgu, g0 + units, from_f32<kBf16>(u));
 }
 
-// ... and otherwise 256 apart.  `padded` (or nullptr) gets dgu with rows of `pitch`
-// values, the ones behind the row's end zeros.
-template <int ACT>
+// ... and otherwise one (n odd) or two at a time, 256 threads' apart.  `padded` (or
+// nullptr) gets dgu with rows of `pitch` values, the ones behind the row's end zeros.
+template <int ACT, typename V>  // V: uint16_t, or uint32_t for two values
 __global__ __launch_bounds__(256) void gate_grad_any_kernel(MxGateGrad G, uint32_t chunks, int64_t first,
                                                             uint16_t* padded, int64_t pitch) {
-  const int64_t at = first + blockIdx.x, row = at / chunks, n = G.n;
-  const int64_t c0 = (at - row * chunks) * 2048 + threadIdx.x;
-  const uint16_t* const dh = G.dh + row * n;
-  const uint16_t* const gu = G.gu + 2 * row * n;
-  uint16_t* const dgu = G.dgu + 2 * row * n;
-  uint16_t* const pad = padded + row * pitch;
-  uint16_t x[8], g[8], u[8];
+  constexpr int W = sizeof(V) / 2, E = 8 / W;
+  const int64_t row = first + blockIdx.x / chunks, n = G.n / W;
+  const int64_t c0 = (int64_t)(blockIdx.x % chunks) * (2048 / W) + threadIdx.x;
+  const V* const dh = reinterpret_cast<const V*>(G.dh + row * G.n);
+  const V* const gu = reinterpret_cast<const V*>(G.gu + 2 * row * G.n);
+  V* const dgu = reinterpret_cast<V*>(G.dgu + 2 * row * G.n);
+  V* const pad = reinterpret_cast<V*>(padded + row * pitch);
+  V x[E], g[E], u[E];
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < E; ++i) {
     const int64_t c = c0 + 256 * i < n ? c0 + 256 * i : n - 1;
     x[i] = dh[c];
     g[i] = gu[c];
     u[i] = gu[n + c];
   }
 #pragma unroll
-  for (int i = 0; i < 8; ++i) {
+  for (int i = 0; i < E; ++i) {
     const int64_t c = c0 + 256 * i;
     if (c >= n) continue;
-    float dg, du;
-    gate_grad<ACT>(bf16_bits_to_f32(x[i]), bf16_bits_to_f32(g[i]), bf16_bits_to_f32(u[i]), dg, du);
-    const uint16_t a = (uint16_t)f32_to_bf16_bits(dg), b = (uint16_t)f32_to_bf16_bits(du);
+    V a = 0, b = 0;
+#pragma unroll
+    for (int w = 0; w < W; ++w) {
+      auto value = [&](uint32_t v) { return bf16_bits_to_f32(v >> (16 * w) & 0xFFFFu); };
+      float dg, du;
+      gate_grad<ACT>(value(x[i]), value(g[i]), value(u[i]), dg, du);
+      a |= (V)(f32_to_bf16_bits(dg) << (16 * w));
+      b |= (V)(f32_to_bf16_bits(du) << (16 * w));
+    }
     dgu[c] = a;
     dgu[n + c] = b;
     if (padded) {
       pad[c] = a;
       pad[n + c] = b;
-      if (c < pitch - 2 * n) pad[2 * n + c] = 0;  // (at most 7)
+      if (c < pitch / W - 2 * n) pad[2 * n + c] = 0;  // (at most 7 values)
     }
   }
 }
@@ -78,8 +85,7 @@ __global__ __launch_bounds__(256) void gate_grad_any_kernel(MxGateGrad G, uint32
 // rows of n values to rows of `pitch`, zeros behind
 __global__ __launch_bounds__(256) void pad_kernel(const uint16_t* x, int64_t n, uint16_t* y, int64_t pitch,
                                                   uint32_t chunks, int64_t first) {
-  const int64_t at = first + blockIdx.x, row = at / chunks;
-  const int64_t c0 = (at - row * chunks) * 2048 + threadIdx.x;
+  const int64_t row = first + blockIdx.x / chunks, c0 = (int64_t)(blockIdx.x % chunks) * 2048 + threadIdx.x;
   uint16_t v[8];
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -91,13 +97,13 @@ __global__ __launch_bounds__(256) void pad_kernel(const uint16_t* x, int64_t n, 
     if (c0 + 256 * i < pitch) y[row * pitch + c0 + 256 * i] = v[i];
 }
 
-// f(chunks, first, grid) over launches of at most 2^23 blocks: rows of n values in
-// chunks of 2048
+// f(chunks, first row, grid) over launches of at most 2^23 blocks (or one row): rows of
+// n values in chunks of 2048
 template <typename F>
 hipError_t over_rows(int64_t rows, int64_t n, F&& f) {
-  const int64_t chunks = (n + 2047) / 2048;
-  return in_parts(rows * chunks, INT64_C(1) << 23, [&](int64_t first, int64_t count) {
-    f((uint32_t)chunks, first, dim3((uint32_t)count));
+  const int64_t chunks = (n + 2047) / 2048, most = (INT64_C(1) << 23) / chunks;
+  return in_parts(rows, most > 0 ? most : 1, [&](int64_t first, int64_t count) {
+    f((uint32_t)chunks, first, dim3((uint32_t)(count * chunks)));
     return hipGetLastError();
   });
 }
@@ -140,7 +146,10 @@ hipError_t launch_mx_gated_grad(const MxGateGrad& g, const MxBf16Problem& p, hip
   auto any = [&](uint16_t* rows, int64_t pitch) {
     return with_activation(g.act, [&](auto ACT) {
       return over_rows(g.m, g.n, [&](uint32_t chunks, int64_t first, dim3 grid) {
-        gate_grad_any_kernel<decltype(ACT)::value><<<grid, dim3(256), 0, stream>>>(g, chunks, first, rows, pitch);
+        if (g.n % 2 == 0)
+          gate_grad_any_kernel<decltype(ACT)::value, uint32_t><<<grid, dim3(256), 0, stream>>>(g, chunks, first, rows, pitch);
+        else
+          gate_grad_any_kernel<decltype(ACT)::value, uint16_t><<<grid, dim3(256), 0, stream>>>(g, chunks, first, rows, pitch);
       });
     });
   };

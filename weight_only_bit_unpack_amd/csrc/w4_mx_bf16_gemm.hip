@@ -330,18 +330,19 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
 #pragma unroll
     for (int i = 0; i < MT; ++i) multiply_row(o, v, i);
   };
-  // A quarter's products with the next one's reads and rebuilding between them:
-  // left alone, the compiler puts the reads behind the products and waits for
-  // them before the next.
+  // Forward, a quarter's products with the next one's reads and rebuilding between
+  // them: left alone, the compiler puts the reads behind the products and waits for
+  // them before the next (4096 x 22016 x 4096 594 against 587 us).  Backward, where the
+  // LDS has more to do, its order is the better one (563 against 584).
   auto interleave = [&]() {
-    constexpr int products = 2 * MT, reads = MT + (kBack ? 4 : 0), valu = 8 / products + 1;
+    if constexpr (!kBack) {
+      constexpr int products = 2 * MT, valu = 8 / products + 1;
 #pragma unroll
-    for (int n = 0; n < products; ++n) {
-#pragma unroll
-      for (int m = n * reads / products; m < (n + 1) * reads / products; ++m)
-        __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
-      __builtin_amdgcn_sched_group_barrier(0x002, valu, 0);
+      for (int n = 0; n < products; ++n) {
+        if (n < MT) __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x002, valu, 0);
+      }
     }
     __builtin_amdgcn_sched_barrier(0);
   };
