@@ -89,6 +89,24 @@ def test_more_than_a_launch(lib):
     assert lib.w4_mx_gated_linear_grad(0, 32, n, A, A, A, A, m, A, A, 1, None) == SHAPE
 
 
+def test_every_kernel_is_taken_by_some_product(lib):
+    """Each tile, whole and with its last ones in parts, and each few-row shape, on the
+    card's 256 compute units."""
+    i32, i64 = ctypes.c_int32, ctypes.c_int64
+    f = lib.w4_mx_bf16_kernel_of
+    f.argtypes, f.restype = [i32, i64, i64, i64], i32
+    ms = [1, 16, 17, 64, 130, 333, 700, 1500, 2050, 4100]
+    ns = [96, 513, 1100, 2730, 4100, 5500, 11008, 33000]
+    ks = [64, 256, 1024, 2272, 4096, 11008, 32768]
+    for kind in (0, 1, 2):
+        seen = {f(kind, n, k, m) for m in ms for n in ns for k in ks}
+        plain, cut = {s for s in seen if s < 1024}, {s - 1024 for s in seen if 1024 <= s < 4096}
+        assert {s % 16 for s in plain} == set(range(5)), kind
+        assert {s // 16 for s in plain} >= {1, 2, 3, 4, 6, 8, 12}, kind
+        assert {s % 16 for s in cut} >= {0, 2}, kind
+        assert {s - 4096 for s in seen if s >= 4096} == (set() if kind == 2 else {0, 1, 2}), kind
+
+
 @pytest.mark.skipif(shutil.which("g++") is None or not os.path.isdir("/opt/rocm/include"),
                     reason="needs g++ and the HIP headers")
 def test_validation_under_sanitizers(tmp_path):

@@ -642,8 +642,10 @@ struct Plan {
 int64_t outputs(const MxBf16Problem& p) { return p.kind == kMxBackward ? p.k : p.n; }
 int64_t steps_of(const MxBf16Problem& p) { return ((p.kind == kMxBackward ? p.n : p.k) + 63) / 64; }
 
-// Tiles that are cut at most: their counts have a place of their own.
-constexpr int64_t kMaxCut = kMxCounters;
+// Tiles that are cut at most (their counts have a place each), and parts that they are
+// cut into at most (256 MB of sums on the largest tile; more than four blocks a CU are
+// not worth their joining).
+constexpr int64_t kMaxCut = kMxCounters, kMaxParts = 1024;
 
 // Tile number t, the tiles from `whole` on in s parts (s == 1: none); tile < 0
 // where they do not fit the problem: a tile's rows of x and of outputs stay below
@@ -657,9 +659,9 @@ Plan plan_on(const MxBf16Problem& p, int t, uint32_t s, int64_t whole) {
   if (s == 1) q.whole = tiles;
   constexpr int64_t kTileBytes = (INT64_C(1) << 31) - 1;
   if (4 * wide > kTileBytes / T::BM || 2 * p.x_pitch > kTileBytes / T::BM) q.tile = -1;
-  if (q.whole > tiles || (int64_t)s > steps_of(p) || (s > 1 && q.cut() > kMaxCut)) q.tile = -1;
+  if (q.whole > tiles || (int64_t)s > steps_of(p) || (s > 1 && (q.cut() > kMaxCut || q.cut() * s > kMaxParts))) q.tile = -1;
   if (std::is_same_v<T, T4> && p.kind == kMxBackward && s > 1 && q.whole > 0) q.tile = -1;  // (all tiles or none)
-  if ((tiles * s + 14) * T::THREADS > kMaxLaunchThreads) q.tile = -1;
+  if ((tiles + kMaxParts + 14) * T::THREADS > kMaxLaunchThreads) q.tile = -1;
   return q;
 }
 
@@ -774,10 +776,10 @@ bool skinny(const MxBf16Problem& p) { return p.m <= 16 && p.kind != kMxBackward;
 }  // namespace
 
 bool mx_bf16_fits(const MxBf16Problem& p) {
-  // No tile is smaller than 32 x 64 outputs or has more than 512 threads: where a
-  // launch holds the blocks of that, it holds any plan's, and the costs are
-  // computed by the launch only.
-  if (((p.m + 31) / 32 * ((outputs(p) + 63) / 64) * kMaxSplits + 14) * 512 <= kMaxLaunchThreads) return true;
+  // No tile is smaller than 32 x 32 outputs or has more than 512 threads, and the
+  // few-row kernels have fewer blocks: where a launch holds the blocks of that, it
+  // holds any plan's, and the costs are computed by the launch only.
+  if (((p.m + 31) / 32 * ((outputs(p) + 31) / 32) + kMaxParts + 14) * 512 <= kMaxLaunchThreads) return true;
   return make_plan(p).blocks() <= 0x7FFFFFFF;
 }
 
