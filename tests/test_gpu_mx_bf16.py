@@ -393,6 +393,25 @@ def test_empty_sizes(w4):
     assert dx.shape == (0, 64) and dgu.shape == (0, 6)
 
 
+@pytest.mark.parametrize("n", [1, 2, 3, 5, 6, 7, 9, 10])
+def test_padding_does_not_reach_the_sums(w4, n):
+    """The rows that the call pads lie in memory where an earlier call left NaN."""
+    report("mx_bf16_padding", n=n)
+    g = np.random.default_rng(n)
+    wq, ws, w = exact_weight(g, 2 * n, 64)
+    m = 40
+    nans = torch.full((2 * m, 101), float("nan"), dtype=BF16, device="cuda")
+    w4.w4_mx_linear_grad(nans, *exact_weight(g, 101, 64)[:2])
+    dh, gu = dev(g.standard_normal((m, n))), dev(g.standard_normal((m, 2 * n)))
+    dx, dgu = w4.w4_mx_gated_linear_grad(dh, gu, wq, ws, w4.W4_GELU, dx_dtype=F32)
+    assert bool(torch.isfinite(dx).all())
+    limit = 2 * 2 * n * E * (np.abs(f64(dgu)) @ np.abs(w)) + 2.0 ** -149
+    assert (np.abs(f64(dx) - f64(dgu) @ w) <= limit).all()
+    w4.w4_mx_linear_grad(nans, *exact_weight(g, 101, 64)[:2])
+    dy = exact_rows(g, m, n)
+    same(w4.w4_mx_linear_grad(dev(dy), wq[:n], ws[:n], dx_dtype=F32), dy @ w[:n])
+
+
 # ------------------------------------------------------------------ together, streams, graphs
 def block(w4, x, dy, up, down, act, gu, stream=None):
     """A feed-forward block and its backward pass: (y, dx)."""

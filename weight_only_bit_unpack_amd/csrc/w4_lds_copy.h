@@ -31,6 +31,11 @@ __device__ __forceinline__ void copy_byte(const uint8_t* from, uint32_t to) {
   asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, off" ::"s"(to), "v"(from)
                : "memory");
 }
+__device__ __forceinline__ void copy_byte(const uint8_t* base, uint32_t offset, uint32_t to) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_ubyte %1, %2" ::"s"(to), "v"(offset),
+               "s"(base)
+               : "memory");
+}
 
 // s_waitcnt for at most n vector memory operations in flight, the others free.
 constexpr int wait_vm(int n) { return (n & 15) | (n >> 4) << 14 | 0x0F70; }

@@ -62,6 +62,7 @@ __global__ __launch_bounds__(256) void gate_grad_any_kernel(MxGateGrad G, uint32
 #pragma unroll
   for (int i = 0; i < E; ++i) {
     const int64_t c = c0 + 256 * i;
+    if (padded && c < pitch / W - 2 * n) pad[2 * n + c] = 0;  // (at most 7 values, maybe more than n)
     if (c >= n) continue;
     V a = 0, b = 0;
 #pragma unroll
@@ -77,7 +78,6 @@ __global__ __launch_bounds__(256) void gate_grad_any_kernel(MxGateGrad G, uint32
     if (padded) {
       pad[c] = a;
       pad[n + c] = b;
-      if (c < pitch / W - 2 * n) pad[2 * n + c] = 0;  // (at most 7 values)
     }
   }
 }

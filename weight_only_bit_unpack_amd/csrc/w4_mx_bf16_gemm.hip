@@ -39,9 +39,17 @@ typedef short i16x4 __attribute__((ext_vector_type(4)));
 // the steps of 64 in turn, each with LDS of its own: where there are too few
 // tiles to give a SIMD two waves otherwise, its instructions' latencies are the
 // bound.  NS (backward: NB) steps of a group in LDS: one read, the others arriving.
-template <int BM_, int BN_, int WM_, int WN_, int WK_, int NS_, int NB_>
+//
+// LC > 0: forward, the scales of LC steps of every group come at once, copied by the
+// whole block: then a copy reads eight neighbouring bytes of eight rows, not two of
+// 32 rows with a line each, which keep the cache busy longer than the waves where two
+// of them share a SIMD (1024 x 4096 x 4096 on T1 44.1 instead of 49.7 us, 333 x 5504 x
+// 4096 on T3 29.9, 36.5).  Where a wave is alone there, or power is the bound, the extra
+// instructions cost more (333 x 5504 x 4096 on T2 34.4, 31.0; 2048 x 4096 x 11008 on T0
+// 205, 192; T4 within 2%).
+template <int BM_, int BN_, int WM_, int WN_, int WK_, int NS_, int NB_, int LC_ = 0>
 struct Tile {
-  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, WK = WK_, NS = NS_, NB = NB_;
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, WK = WK_, NS = NS_, NB = NB_, LC = LC_;
   static constexpr int NW = WM * WN, THREADS = 64 * NW * WK, MT = BM / WM / 32;
   static_assert(BN == 64 * WN && BM == 32 * WM * MT, "waves of 32 MT x 64");
   // 16-byte units of a step: rows of x, weights, scale bytes (a dword each)
@@ -49,15 +57,19 @@ struct Tile {
   static constexpr int R = BN * 8;  // backward: 64 rows of BN rebuilt weights
   static constexpr int IA = A / (64 * NW), IW = W / (64 * NW), IS = 4 * S / (64 * NW);  // copies of a wave
   static_assert(IA * 64 * NW == A && IW * 64 * NW == W && IS == IW, "the waves share the copies");
-  static constexpr int COPIES = IA + IW + IS;
-  static constexpr int FORWARD = NS * (A + W + S), BACKWARD = NB * (A + W + S) + 2 * R;  // units of a group's LDS
-  static_assert(WK * FORWARD < 10240 && WK * BACKWARD < 10240, "the LDS of a CU");
+  // a chunk of scales: blocks, units, copies of a wave
+  static constexpr int SC = LC > 0 ? 2 * WK * LC : 8, C = LC > 0 ? BN * SC / 4 : 0, IC = C / (16 * NW * WK);
+  static_assert(LC == 0 || (NS <= LC + 1 && IC * 16 * NW * WK == C), "what a chunk overwrites is read; waves share");
+  // units of a group's LDS, and of a block's
+  static constexpr int FORWARD = NS * (A + W + (LC > 0 ? 0 : S)), BACKWARD = NB * (A + W + S) + 2 * R;
+  static constexpr int ALL_FORWARD = WK * FORWARD + 2 * C, ALL_BACKWARD = WK * BACKWARD;
+  static_assert(ALL_FORWARD < 10240 && ALL_BACKWARD < 10240, "the LDS of a CU");
   static_assert((WK - 1) * BM * BN / 4 <= WK * FORWARD, "the groups' sums fit in it");
 };
 using T0 = Tile<256, 256, 2, 4, 1, 3, 2>;
-using T1 = Tile<128, 256, 2, 4, 1, 3, 3>;
+using T1 = Tile<128, 256, 2, 4, 1, 3, 3, 4>;
 using T2 = Tile<128, 128, 2, 2, 1, 3, 2>;
-using T3 = Tile<64, 128, 2, 2, 2, 3, 2>;
+using T3 = Tile<64, 128, 2, 2, 2, 3, 2, 2>;
 using T4 = Tile<32, 64, 1, 1, 4, 3, 2>;  // (backward: the narrow kernel, whose tiles are the same)
 constexpr int kTiles = 5;
 
@@ -91,15 +103,18 @@ __device__ __forceinline__ int swizzle_w(int row) { return (row >> 3) & 1; }
 template <int BN>
 __device__ __forceinline__ int swizzle_r(int row, int c) {
   const int n0 = row & 1, n1 = (row >> 1) & 1, c3 = (c >> 3) & 1, c4 = (c >> 4) & 1;
-  if constexpr (BN == 256) return c ^ (n1 << 3 | n0 << 2 | (n0 ^ c3) << 1 | c4);
-  if constexpr (BN == 128) return c ^ (n1 << 3 | n0 << 2 | (n0 ^ c3) << 1 | n1);
-  return c ^ (n1 << 2 | n1 << 1 | n0);
+  static_assert(BN == 256 || BN == 128, "the tiles of the backward products");
+  return c ^ (n1 << 3 | n0 << 2 | (n0 ^ c3) << 1 | (BN == 256 ? c4 : n1));
 }
 
 template <int KIND, typename T>
 __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem P, GemmArgs G) {
   constexpr bool kBack = KIND == kMxBackward, kGate = KIND == kMxGated;
-  constexpr int MT = T::MT, NS = kBack ? T::NB : T::NS;
+  constexpr bool kChunks = !kBack && T::LC > 0;
+  constexpr int MT = T::MT, NS = kBack ? T::NB : T::NS, SC = T::SC, LC = kChunks ? T::LC : 1;
+  // of a wave and step (a chunk's come before those of its first step, so that a wait
+  // that counts without them waits for them too)
+  constexpr int kCopies = T::IA + T::IW + (kChunks ? 0 : T::IS);
   constexpr int U = T::BN / 32;                        // backward: units of a weight row in the tile
   constexpr int OUT = kGate ? T::BN / 2 : T::BN;       // outputs of a row in the tile
   extern __shared__ u32x4 lds[];
@@ -142,6 +157,7 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
   auto slot_a = [&](uint32_t s) { return base + s * T::A; };
   auto slot_w = [&](uint32_t s) { return base + NS * T::A + s * T::W; };
   auto slot_s = [&](uint32_t s) { return base + NS * (T::A + T::W) + s * T::S; };
+  auto slot_c = [&](uint32_t c) { return T::WK * T::FORWARD + (c & 1) * T::C; };  // chunk c of scales
   auto slot_r = [&](uint32_t i) { return base + NS * (T::A + T::W + T::S) + (i & 1) * T::R; };
   const uint32_t lds0 = lds_address(lds);
 
@@ -194,13 +210,41 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
 #pragma unroll
   for (int i = 0; i < T::IS; ++i) {
     const int u = (wave * T::IS + i) * 64 + lane;
-    if constexpr (kBack) {
+    if constexpr (kChunks) {
+      sp[i] = nullptr;
+    } else if constexpr (kBack) {
       const uint32_t c = (uint32_t)(n0 >> 5) + u % U;
       sp[i] = P.w_scales + (int64_t)(u / U) * blocks + (c < blocks ? c : blocks - 1);
     } else {
       sp[i] = P.w_scales + weight_row(u >> 1) * blocks + (u & 1);
     }
   }
+  // Chunk c: dword p of a row's SC holds block p ^ swizzle_c(row) of it, so that the
+  // reads of 32 rows and two blocks take all banks.
+  auto swizzle_c = [](int row) { return row / (64 / SC) % (SC / 2) * 2; };
+  const uint8_t* const cb = uniform(P.w_scales + n0 * (int64_t)blocks + 2 * t0);
+  uint32_t cv[kChunks ? T::IC : 1];  // (a tile's rows: at most 256 of 2^17 bytes; not the way to the up rows)
+  if constexpr (kChunks) {
+#pragma unroll
+    for (int i = 0; i < T::IC; ++i) {
+      const int row = ((waves * T::IC + i) * 64 + lane) / SC;
+      const int c = kGate ? (row >> 6) * 32 + (row & 31) : (row & ~63) + 2 * (row & 31) + ((row >> 5) & 1);
+      cv[i] = (uint32_t)(c < cols_n ? c : cols_n - 1) * blocks + ((lane % SC) ^ swizzle_c(row));
+    }
+  }
+  auto copy_chunk = [&](uint32_t c) {
+    const uint32_t b0 = 2 * t0 + SC * c;
+#pragma unroll
+    for (int i = 0; i < T::IC; ++i) {
+      const int at = (waves * T::IC + i) * 64;  // (rows of one half of 64)
+      const uint8_t* const from = uniform(cb + SC * c + (kGate ? (at / SC >> 5 & 1) * (P.n * blocks) : 0));
+      const uint32_t to = lds0 + 16 * slot_c(c) + 4 * at;
+      if (32 * (b0 + SC) <= end)
+        copy_byte(from, cv[i], to);
+      else
+        copy_byte(32 * (b0 + ((lane % SC) ^ swizzle_c((at + lane) / SC))) < end ? from + cv[i] : zeros, to);
+    }
+  };
   const int64_t step_w = kBack ? 64 * (int64_t)half : 32, step_s = kBack ? 64 * (int64_t)blocks : 2;
   auto inside = [&](uint32_t t, int at) {  // row or block `at` of step t lies before the end of the sum
     return 64 * t + (kBack ? 1 : 32) * at < end;
@@ -216,16 +260,20 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
       if (!whole) from = inside(t, at_w(lane, c)) ? from : zeros;
       copy16(from, lds0 + 16 * (slot_w(s) + (wave * T::IW + c) * 64));
     }
+    if constexpr (!kChunks) {
 #pragma unroll
-    for (int c = 0; c < T::IS; ++c) {
-      const uint8_t* from = sp[c] + t * step_s;
-      if (!whole) from = inside(t, at_s(lane, c)) ? from : zeros;
-      copy_byte(from, lds0 + 16 * slot_s(s) + (wave * T::IS + c) * 256);
+      for (int c = 0; c < T::IS; ++c) {
+        const uint8_t* from = sp[c] + t * step_s;
+        if (!whole) from = inside(t, at_s(lane, c)) ? from : zeros;
+        copy_byte(from, lds0 + 16 * slot_s(s) + (wave * T::IS + c) * 256);
+      }
     }
   };
   // step i to ring slot s (backward: with the weights of step i + 1, to the next slot)
   auto copy = [&](uint32_t i, uint32_t s, auto WHOLE) {
     const uint32_t t = step_at(i);
+    if constexpr (kChunks)
+      if (i % LC == 0) copy_chunk(i / LC);
     const uint32_t to_a = lds0 + 16 * (slot_a(s) + wave * T::IA * 64);
     const uint8_t* const xs = uniform(xb + (uint64_t)t * 128);
 #pragma unroll
@@ -264,13 +312,17 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
   struct Weights {
     u32x4 b[2];
   };
-  auto read_step = [&](Step& v, uint32_t s) {
+  auto read_step = [&](Step& v, uint32_t s, uint32_t i) {
     if constexpr (!kBack) {
 #pragma unroll
       for (int j = 0; j < 2; ++j) {
         const int row = wn * 64 + 32 * j + r;
         v.w[j] = lds[slot_w(s) + 2 * row + (h ^ swizzle_w(row))];
-        v.s[j] = reinterpret_cast<const uint32_t*>(lds + slot_s(s))[2 * row + h];
+        if constexpr (kChunks)
+          v.s[j] = reinterpret_cast<const uint32_t*>(
+              lds + slot_c(i / LC))[row * SC + ((2 * T::WK * (i % LC) + 2 * group + h) ^ swizzle_c(r))];
+        else
+          v.s[j] = reinterpret_cast<const uint32_t*>(lds + slot_s(s))[2 * row + h];
       }
     }
   };
@@ -317,10 +369,12 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
     v.s = reinterpret_cast<const uint32_t*>(lds + slot_s(s))[u];
   };
   auto rebuild_unit = [&](const Unit& v, uint32_t n, int i) {
-    const int u = (wave * T::IW + i) * 64 + lane, row = u / U, c = u % U;
+    if constexpr (kBack) {
+      const int u = (wave * T::IW + i) * 64 + lane, row = u / U, c = u % U;
 #pragma unroll
-    for (int e = 0; e < 4; ++e)
-      lds[slot_r(n) + row * (T::BN / 8) + swizzle_r<T::BN>(row, 4 * c + e)] = mx_rebuild8(v.w[e], v.s);
+      for (int e = 0; e < 4; ++e)
+        lds[slot_r(n) + row * (T::BN / 8) + swizzle_r<T::BN>(row, 4 * c + e)] = mx_rebuild8(v.w[e], v.s);
+    }
   };
   auto multiply_row = [&](const Quarter& o, const Weights& v, int i) {
 #pragma unroll
@@ -389,11 +443,11 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
     if (fast || n + 1 < count) {
       // the next step's copies: all but those of the NS - 2 steps after it
       if (fast || n + NS <= count)
-        __builtin_amdgcn_s_waitcnt(wait_vm((NS - 2) * T::COPIES));
+        __builtin_amdgcn_s_waitcnt(wait_vm((NS - 2) * kCopies));
       else
         __builtin_amdgcn_s_waitcnt(wait_vm(0));
       lds_barrier();
-      read_step(st, next);
+      read_step(st, next, n + 1);
       read(o0, next, Q0{});
       if constexpr (kBack) weights(b0, st, n + 1, Q0{});
       __builtin_amdgcn_sched_barrier(0);
@@ -419,7 +473,7 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
       // these copies bring weights to the slot of t0's, which are rebuilt first
       // (behind a barrier: nothing else keeps their reads below the wait)
       if (NS - 1 <= count)
-        __builtin_amdgcn_s_waitcnt(wait_vm((NS - 1) * T::COPIES));
+        __builtin_amdgcn_s_waitcnt(wait_vm((NS - 1) * kCopies));
       else
         __builtin_amdgcn_s_waitcnt(wait_vm(0));
       lds_barrier();
@@ -434,11 +488,11 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
     if (i < count) copy(i, i, std::false_type{});
   }
   if (NS <= count)
-    __builtin_amdgcn_s_waitcnt(wait_vm((NS - 1) * T::COPIES));
+    __builtin_amdgcn_s_waitcnt(wait_vm((NS - 1) * kCopies));
   else
     __builtin_amdgcn_s_waitcnt(wait_vm(0));
   lds_barrier();
-  read_step(st, 0);
+  read_step(st, 0, 0);
   read(o0, 0, Q0{});
   weights(b0, st, 0, Q0{});
   const uint32_t fast = whole < count ? whole : count;  // steps n with n + NS < fast
@@ -488,7 +542,7 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
         const f32x16& a = acc[v / 16][v / 8 % 2];
         return (f32x2){a[v % 8 * 2], a[v % 8 * 2 + 1]};
       });
-    if (!last_part(G.counted + (tile - G.whole), splits) || !lead) return;
+    if (!last_part(G.counted + (tile - G.whole), splits, reinterpret_cast<uint32_t*>(lds)) || !lead) return;
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
@@ -728,7 +782,7 @@ Plan make_plan(const MxBf16Problem& p) {
 
 template <int KIND, typename T>
 hipError_t launch_tile(const MxBf16Problem& p, const GemmArgs& g, uint32_t blocks, hipStream_t stream) {
-  constexpr int lds = 16 * T::WK * (KIND == kMxBackward ? T::BACKWARD : T::FORWARD);
+  constexpr int lds = 16 * (KIND == kMxBackward ? T::ALL_BACKWARD : T::ALL_FORWARD);
   // the LDS limit is raised once per device (one bit each for the first 64);
   // callers racing here all set the same value
   static std::atomic<uint64_t> configured{0};

@@ -172,7 +172,7 @@ __global__ __launch_bounds__(kThreads) void mx_bf16_narrow_kernel(MxBf16Problem 
       const f32x4& s = sum[i / 2];
       return (f32x2){s[i % 2 * 2], s[i % 2 * 2 + 1]};
     });
-    if (!last_part(G.counted + tile, G.splits)) return;
+    if (!last_part(G.counted + tile, G.splits, reinterpret_cast<uint32_t*>(lds))) return;
     add_parts<4, 16>(parts, 4 * kThreads, kThreads, G.splits, [&](int i, const f32x2& x) {
       sum[i / 2][i % 2 * 2] = x.x;
       sum[i / 2][i % 2 * 2 + 1] = x.y;

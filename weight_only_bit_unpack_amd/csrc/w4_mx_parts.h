@@ -22,17 +22,16 @@ __device__ __forceinline__ void put_part(uint64_t* at, int stride, F&& get) {
 }
 
 // Every thread of the block calls this when its part is put; true in the block
-// that is the last of `splits`, whose count is then back at zero.
-__device__ __forceinline__ bool last_part(uint32_t* counted, uint32_t splits) {
-  __shared__ uint32_t before;
+// that is the last of `splits`, whose count is then back at zero.  `before` is a dword of
+// LDS that nobody reads or writes any more.
+__device__ __forceinline__ bool last_part(uint32_t* counted, uint32_t splits, uint32_t* before) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   if (threadIdx.x == 0) {
-    before = __hip_atomic_fetch_add(counted, 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-    if (before + 1 == splits) __hip_atomic_store(counted, 0u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    *before = atomicInc(counted, splits - 1);  // (after splits - 1 comes 0)
   }
   __syncthreads();
-  return before + 1 == splits;
+  return *before + 1 == splits;
 }
 
 // set(v, sum of pair v over the parts, in order): part p's at from[p * part + v *
