@@ -32,7 +32,7 @@
  *    error return nothing is enqueued and no output byte changes.  Faults in
  *    the kernels surface at the caller's next synchronisation.
  *  - Results are deterministic: the same inputs give the same output bits
- *    (fixed reduction order, no atomics).
+ *    (fixed reduction order; atomics only count which parts of a sum are done).
  *  - Weights are row-major [n][k] (n = output features, k = input features,
  *    the layout of a PyTorch Linear weight).  A group is `group` consecutive
  *    weights along k; k must be a multiple of the codec's group (64, or 32
@@ -569,26 +569,29 @@ w4_status w4_mx_grouped_linear(int32_t x_format, int32_t experts, int64_t n, int
  * around frozen 4-bit weights.  W_hat, the weight's values, are those that
  * w4_mx_dequant gives as bf16 (NaN in a block of scale 255).
  *
- * Conventions of the four calls: sums are fp32, in the matrix core; bf16
- * products are exact in fp32, so an fp32 output is within (terms / 16 + 40) *
- * 2^-24 of the sum of the products' magnitudes, and a bf16 output (RNE) within
- * 2^-9 |y| more.  The same inputs give the same bits, also with other rows
- * beside them as long as m stays the same.  A NaN or an infinity in a row of x (or
- * of dy) reaches that row's outputs only, one in a weight its row's (backward:
- * its columns') only.  k % 32 == 0; any other size, m included, may be 0: an empty
- * sum is +0, an empty output nothing to do.
+ * Conventions of the four calls: products are exact and sums fp32, in the matrix
+ * core, so that an fp32 output is within 2 terms * 2^-24 of the sum of the products'
+ * magnitudes whatever the order of the additions (on normal data 6e-8 of the result
+ * in the 2-norm at 5632 terms, as an fp32 product's), and a bf16 output (RNE) within 2^-8
+ * |y| more.  The same inputs give the same bits; a row's outputs depend on the number
+ * of rows beside it, which chooses the kernel, and not on what they hold.  A NaN or an
+ * infinity in a row of x (or of dy) reaches that row's outputs only, one in a weight its
+ * row's (backward: its columns') only.  k % 32 == 0; any other size, m included, may be
+ * 0: an empty sum is +0, an empty output nothing to do.
  * x, dy, dh, gu (where read), dgu and w, w_scales 16-byte aligned; y and dx 4-byte
  * (fp32) or 2-byte (bf16) aligned, as is gu where it is written.
  * Errors: W4_EINVAL (bad activation, negative size, null pointer), W4_ESHAPE
  * (k % 32 != 0, k above W4_MAX_MATMUL_K, more than W4_MAX_MX_N rows of the weight,
  * m above 2^31 - 1, more tiles than 2^32 threads work on), W4_EALIGN,
  * W4_EUNSUPPORTED (output dtype), W4_EHIP.
- * Workspace: a product with few output tiles may split its sum into S <= 8 parts
- * and enqueue a second kernel that adds them in order, S * 4 bytes per sum; a
- * backward product whose summed length (n; gated 2 n) is not a multiple of 8
- * first copies its rows, 2 bytes a value, padded to one.  Both are kept per
- * (device, stream) exactly as for w4_gemm (see there, also for capture into a
- * graph).
+ * Workspace: where a product's tiles, or those of its last round over the GPU, are too
+ * few, their sums may be cut into at most 1024 parts in all, whose fp32 values (256 KB
+ * of them at most a part) the last block of a tile adds in order; a backward product
+ * whose summed length (n; gated 2 n) is not a multiple of 8 first copies its rows, 2
+ * bytes a value, padded to one.  Both, and 8 KB of counters that every launch leaves at
+ * zero, are kept per (device, stream) exactly as for w4_gemm (see there, also for
+ * capture into a graph: one call of each shape on the capture stream before).  Forward
+ * calls of at most 16 rows use none.
  */
 typedef enum {
   W4_SILU = 0,     /* g / (1 + e^-g) */

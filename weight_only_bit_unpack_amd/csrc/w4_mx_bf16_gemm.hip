@@ -722,13 +722,14 @@ Plan plan_on(const MxBf16Problem& p, int t, uint32_t s, int64_t whole) {
 // What a product costs on a tile: a block alone on its CU takes first + step us for
 // its start and end and per step of a group, two blocks that share one (where they
 // fit) first2 + step2; a launch takes `launch`, and sums in parts take `join` and, for
-// each part, `part` and its bytes at 64 KB a `copy`.  Fitted to 4200 times of every
+// each part, `part` and its bytes at 64 KB a `copy`.  Fitted to 8100 times of every
 // tile and number of parts over 17 to 1500 rows, 300 to 22016 columns and sums of 300
-// to 22016 (root mean square of the error 8 to 10%); the plans they choose take 1.3%
-// more than the best ones on average.  Examples (us, graph replays): 64 x 1000 x 4096
-// 8.5 on tile 4 in four parts, 1 part 12.3, tile 3 in eight parts 12; gated 333 x 2730 x
-// 2080 20.6 on tile 2, 23.4 on tile 3, 24.2 on tile 4; backward 2048 x 4096 x 11008 171
-// on tile 0 with the last round's tiles in two parts, 192 without.
+// to 22016 (root mean square of the error 8 to 9%); the plans they choose take 0.8 to
+// 1.5% more than the best ones on average.  Examples (us, graph replays): 64 x 1000 x
+// 4096 8.6 on tile 4 in four parts, 10.7 in one, 11.7 on tile 3 in four; gated 333 x 2730
+// x 2080 21.0 on tile 2, 22.1 on tile 3 and 19.4 there with the last round's tiles in three
+// parts, 24.2 on tile 4; backward 2048 x 4096 x 11008 171 on tile 0 with the last round's
+// tiles in two parts, 192 without.
 struct Cost {
   float first, step, first2, step2;  // first2 == 0: one block a CU
 };
@@ -737,12 +738,12 @@ struct Costs {
   float launch, join, part, copy;
 };
 constexpr Costs kCosts[3] = {
-    {{{7.85f, 1.03f, 0, 0}, {3.90f, 0.69f, 0, 0}, {2.12f, 0.42f, 7.23f, 0.80f}, {0.89f, 0.64f, 3.23f, 1.23f}, {1.76f, 0.42f, 2.33f, 0.77f}},
-     1.8f, 1.95f, 0.28f, 0.9f},
-    {{{13.0f, 1.08f, 0, 0}, {6.29f, 0.71f, 0, 0}, {3.35f, 0.42f, 7.62f, 0.83f}, {1.12f, 0.66f, 3.60f, 1.23f}, {1.83f, 0.42f, 3.07f, 0.79f}},
-     2.6f, 1.97f, 0.28f, 0.9f},
-    {{{8.43f, 1.32f, 0, 0}, {5.08f, 0.94f, 0, 0}, {3.64f, 0.62f, 9.17f, 0.92f}, {3.40f, 0.80f, 0, 0}, {2.14f, 0.78f, 2.78f, 1.37f}},
-     0.6f, 2.23f, 0.11f, 1.0f}};
+    {{{8.41f, 1.05f, 0, 0}, {5.22f, 0.62f, 0, 0}, {2.95f, 0.42f, 7.50f, 0.82f}, {2.18f, 0.55f, 4.51f, 0.95f}, {2.48f, 0.42f, 2.79f, 0.78f}},
+     1.2f, 2.06f, 0.25f, 0.90f},
+    {{{13.7f, 1.09f, 0, 0}, {7.78f, 0.64f, 0, 0}, {4.32f, 0.43f, 8.03f, 0.84f}, {2.65f, 0.55f, 4.81f, 0.98f}, {2.72f, 0.42f, 3.32f, 0.80f}},
+     1.7f, 2.10f, 0.26f, 0.87f},
+    {{{8.56f, 1.32f, 0, 0}, {5.18f, 0.94f, 0, 0}, {3.89f, 0.62f, 9.50f, 0.91f}, {3.49f, 0.80f, 0, 0}, {2.26f, 0.78f, 2.88f, 1.37f}},
+     0.5f, 2.26f, 0.11f, 0.99f}};
 
 Plan make_plan(const MxBf16Problem& p) {
   const int64_t cus = device_cus();
@@ -767,9 +768,16 @@ Plan make_plan(const MxBf16Problem& p) {
         if (s > 1 && tiles > cus) q = plan_on<T>(p, t, s, tiles / cus * cus);
         if (q.tile < 0) continue;
         double us = costs.launch + rounds(q.whole, steps_of(p));
-        if (s > 1)
-          us += rounds(q.cut() * s, (steps_of(p) + s - 1) / s) + costs.join +
-                s * (costs.part + costs.copy * T::BM * T::BN / 16384.0);
+        if (s > 1) {
+          // behind an odd number of rounds of whole tiles that leave room beside them, the
+          // parts run beside the last round and slow it down
+          const int64_t steps = (steps_of(p) + s - 1) / s, parts = q.cut() * s;
+          if (c.first2 > 0 && q.whole / cus % 2 == 1)
+            us += (c.step2 - c.step) * (double)((steps + T::WK - 1) / T::WK) + rounds(parts > cus ? parts - cus : 0, steps);
+          else
+            us += rounds(parts, steps);
+          us += costs.join + s * (costs.part + costs.copy * T::BM * T::BN / 16384.0);
+        }
         if (best.tiles_m == 0 || us < least) {
           least = us;
           best = q;
