@@ -187,16 +187,24 @@ constexpr int kLong = 0, kSplit = 1, kWide = 2;
 
 // By the 16-row weight tiles of an output half and the steps of 256 along k.  Four
 // waves share a tile; eight, while tiles are too few to fill the GPU and k is long
-// (not for many rows of an ungated weight, whose LDS then keeps blocks off a CU: 4095 x
-// 5632 at m = 13 7.6 / 6.7 / 15 us); two, each with two tiles, where tiles are many or k is short, so that x and the
-// joining of sums are paid less often.  Measured (us, graph replays, Long / Split /
-// Wide): m = 1, 1024 x 11008 5.2 / 7.0 / 15, 2816 x 2048 3.6 / 3.4 / 5, 11008 x 4096 7.0 /
-// 6.8 / 9.2; m = 16, 32768 x 1024 23 / 12 / 7.2; gated m = 8, 1024 x 11008 10.9 / 12.5 / 20.6,
-// 5632 x 1024 7.7 / 5.4 / 4.4, 11008 x 4096 13.4 / 13.2 / 14.7.
+// (not for many rows of an ungated weight, whose LDS then keeps blocks off a CU); two,
+// each with two tiles, where tiles are many or k is short and a step's rows of x cost
+// as much as its weights, so that they, and the joining of sums, are paid less often.
+// Measured (us, graph replays, Long / Split / Wide): m = 1, 1024 x 11008 5.2 / 7.0 / 15,
+// 2816 x 2048 3.6 / 3.4 / 5.3, 11008 x 4096 7.0 / 6.7 / 9.1, 32768 x 4096 14.3 / 13.6 / 14.6;
+// 5632 x 1024 4.3 / 3.6 / 4.1, 32768 x 1024 10.9 / 7.0 / 5.6; m = 8, 11008 x 1024 7.2 / 4.7 /
+// 4.5, 32768 x 4096 18.9 / 16.7 / 15.6; m = 13, 4095 x 5632 7.3 / 6.5 / 14; m = 16, 11008 x
+// 4096 13.6 / 11.1 / 11.5, 22016 x 2048 21 / 12.9 / 10.4, 32768 x 1024 23 / 12 / 7.2; gated m =
+// 8, 1024 x 11008 10.9 / 12.5 / 21, 5632 x 1024 7.5 / 5.4 / 4.4, 11008 x 4096 13.6 / 13.3 / 14.7,
+// 22016 x 2048 18.8 / 12.9 / 12.7.  Twice the tiles for a wave of Split or Long (gated two
+// of each kind) are no faster than the best of these on any of them.
 int mx_bf16_skinny_shape(const MxBf16Problem& p) {
   const int64_t tiles = (p.n + 15) / 16, steps = (p.k + 255) / 256;
-  if (tiles >= 1536 || (tiles >= 320 && steps <= 4)) return kWide;
-  return tiles <= 256 && steps > 12 && (p.m <= 8 || p.kind == kMxGated) ? kLong : kSplit;
+  const bool gated = p.kind == kMxGated, shorter = steps <= 4;
+  const bool wide = gated || p.m > 8 ? tiles >= (shorter ? 320 : 1024)
+                                     : tiles >= (shorter ? 600 : 1536) && (shorter || p.m > 4);
+  if (wide) return kWide;
+  return tiles <= 256 && steps > 12 && (p.m <= 8 || gated) ? kLong : kSplit;
 }
 
 hipError_t launch_mx_bf16_skinny(const MxBf16Problem& p, int shape, hipStream_t stream) {
