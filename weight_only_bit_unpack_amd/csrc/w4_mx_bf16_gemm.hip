@@ -20,6 +20,7 @@
 // Backward, the sum is over the rows of W, and its 4 bits lie along the other
 // index: a step's weights are rebuilt a step ahead, once for the block, to bf16
 // rows in LDS, and ds_read_b64_tr_b16 gives a lane four rows of one column.
+#include <algorithm>
 #include <atomic>
 #include <type_traits>
 
@@ -721,29 +722,31 @@ Plan plan_on(const MxBf16Problem& p, int t, uint32_t s, int64_t whole) {
 
 // What a product costs on a tile: a block alone on its CU takes first + step us for
 // its start and end and per step of a group, two blocks that share one (where they
-// fit) first2 + step2; a launch takes `launch`, and sums in parts take `join` and, for
-// each part, `part` and its bytes at 64 KB a `copy`.  Fitted to 8100 times of every
-// tile and number of parts over 17 to 1500 rows, 300 to 22016 columns and sums of 300
-// to 22016 (root mean square of the error 8 to 9%); the plans they choose take 0.8 to
-// 1.5% more than the best ones on average.  Examples (us, graph replays): 64 x 1000 x
-// 4096 8.6 on tile 4 in four parts, 10.7 in one, 11.7 on tile 3 in four; gated 333 x 2730
-// x 2080 21.0 on tile 2, 22.1 on tile 3 and 19.4 there with the last round's tiles in three
-// parts, 24.2 on tile 4; backward 2048 x 4096 x 11008 171 on tile 0 with the last round's
-// tiles in two parts, 192 without.
+// fit) first2 + step2; but a step of all blocks together no less than its operations
+// at `rate` (PFLOP/s, tile 0 and the others), which is what the card's power allows.
+// A launch takes `launch`, and sums in parts take `join` and, for each part, `part` and
+// its bytes at 64 KB a `copy`.  Fitted to 8900 times of every tile and number of parts
+// over 17 to 8192 rows, 300 to 22016 columns and sums of 300 to 22016 (root mean square of
+// the error 7.5 to 8%); the plans they choose take 0.7 to 1.4% more than the best ones on
+// average.  Examples (us, graph replays): 64 x 1000 x 4096 8.6 on tile 4 in four parts,
+// 10.7 in one, 11.7 on tile 3 in four; gated 333 x 2730 x 2080 21.0 on tile 2, 22.1 on
+// tile 3 and 19.4 there with the last round's tiles in three parts, 24.2 on tile 4; 2048 x
+// 4096 x 11008 150 on tile 1, 158 on tile 0 in two parts, 192 in one; backward 165 on
+// tile 0 with the last round's tiles in two parts, 185 without, 198 on tile 1.
 struct Cost {
   float first, step, first2, step2;  // first2 == 0: one block a CU
 };
 struct Costs {
   Cost tile[kTiles];
-  float launch, join, part, copy;
+  float launch, join, part, copy, rate[2];
 };
 constexpr Costs kCosts[3] = {
-    {{{8.41f, 1.05f, 0, 0}, {5.22f, 0.62f, 0, 0}, {2.95f, 0.42f, 7.50f, 0.82f}, {2.18f, 0.55f, 4.51f, 0.95f}, {2.48f, 0.42f, 2.79f, 0.78f}},
-     1.2f, 2.06f, 0.25f, 0.90f},
-    {{{13.7f, 1.09f, 0, 0}, {7.78f, 0.64f, 0, 0}, {4.32f, 0.43f, 8.03f, 0.84f}, {2.65f, 0.55f, 4.81f, 0.98f}, {2.72f, 0.42f, 3.32f, 0.80f}},
-     1.7f, 2.10f, 0.26f, 0.87f},
-    {{{8.56f, 1.32f, 0, 0}, {5.18f, 0.94f, 0, 0}, {3.89f, 0.62f, 9.50f, 0.91f}, {3.49f, 0.80f, 0, 0}, {2.26f, 0.78f, 2.88f, 1.37f}},
-     0.5f, 2.26f, 0.11f, 0.99f}};
+    {{{7.20f, 1.03f, 0, 0}, {4.46f, 0.59f, 0, 0}, {2.52f, 0.42f, 6.61f, 0.89f}, {1.79f, 0.55f, 3.95f, 1.01f}, {2.17f, 0.42f, 2.58f, 0.78f}},
+     1.6f, 2.09f, 0.24f, 0.92f, {1.30f, 1.26f}},
+    {{{12.4f, 1.07f, 0, 0}, {7.02f, 0.60f, 0, 0}, {3.92f, 0.42f, 6.90f, 0.93f}, {2.31f, 0.55f, 4.30f, 1.04f}, {2.45f, 0.42f, 3.19f, 0.80f}},
+     2.1f, 2.09f, 0.24f, 0.90f, {1.38f, 1.28f}},
+    {{{8.26f, 1.30f, 0, 0}, {5.07f, 0.95f, 0, 0}, {3.82f, 0.62f, 8.80f, 0.97f}, {3.42f, 0.80f, 0, 0}, {2.19f, 0.78f, 2.83f, 1.37f}},
+     0.5f, 2.26f, 0.11f, 0.99f, {1.29f, 1.32f}}};
 
 Plan make_plan(const MxBf16Problem& p) {
   const int64_t cus = device_cus();
@@ -754,13 +757,17 @@ Plan make_plan(const MxBf16Problem& p) {
     with_tile(t, [&](auto X) {
       using T = decltype(X);
       const Cost& c = costs.tile[t];
+      // us of a block and step of its groups at the rate
+      const double power = T::BM * T::BN * T::WK * 128e-9 / costs.rate[t > 0];
+      auto steps_in = [](int64_t steps) { return (double)((steps + T::WK - 1) / T::WK); };
       // blocks of so many steps each, in rounds over the CUs
       auto rounds = [&](int64_t blocks, int64_t steps) {
-        const double alone = c.first + c.step * (double)((steps + T::WK - 1) / T::WK);
-        if (c.first2 == 0) return (double)((blocks + cus - 1) / cus) * alone;
-        const double pair = c.first2 + c.step2 * (double)((steps + T::WK - 1) / T::WK);
-        const int64_t rest = blocks % (2 * cus);
-        return (double)(blocks / (2 * cus)) * pair + (rest > cus ? pair : rest > 0 ? alone : 0);
+        const bool pairs = c.first2 > 0;
+        const int64_t per = pairs ? 2 * cus : cus, rest = blocks % per;
+        auto round = [&](bool pair, int64_t n) {
+          return (pair ? c.first2 : c.first) + steps_in(steps) * std::max<double>(pair ? c.step2 : c.step, n * power);
+        };
+        return (double)(blocks / per) * round(pairs, per) + (rest > 0 ? round(rest > cus, rest) : 0);
       };
       for (uint32_t s : {1u, 2u, 3u, 4u, 6u, 8u, 12u, 16u}) {
         Plan q = plan_on<T>(p, t, s, 0);
@@ -773,7 +780,8 @@ Plan make_plan(const MxBf16Problem& p) {
           // parts run beside the last round and slow it down
           const int64_t steps = (steps_of(p) + s - 1) / s, parts = q.cut() * s;
           if (c.first2 > 0 && q.whole / cus % 2 == 1)
-            us += (c.step2 - c.step) * (double)((steps + T::WK - 1) / T::WK) + rounds(parts > cus ? parts - cus : 0, steps);
+            us += steps_in(steps) * std::max<double>(c.step2 - c.step, std::min(parts, cus) * power) +
+                  rounds(parts > cus ? parts - cus : 0, steps);
           else
             us += rounds(parts, steps);
           us += costs.join + s * (costs.part + costs.copy * T::BM * T::BN / 16384.0);
