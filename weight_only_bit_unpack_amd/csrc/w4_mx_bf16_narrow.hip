@@ -6,7 +6,8 @@
 // 64 columns and every fourth step of 64 terms, with the loads of two steps in its
 // registers (three and four: the same or slower) and no barrier until the sums are
 // joined; four waves make a block (eight: the same), and where the tiles are still few,
-// blocks share a tile's terms.
+// blocks share a tile's terms.  24 rows of a weight of 11264 x 2048 take 12.0 us in eight
+// parts (37.6 in one, 20.2 on 64 x 128 tiles), 64 of 4096 x 4096 12.1 in two (15.6).
 //
 // The weight's 4 bits lie along the columns, the sum goes over its rows: the 64 rows of
 // a step are rebuilt to bf16 by the lanes that loaded them into 8 KB of the wave's own

@@ -11,6 +11,10 @@
 // waves share their weight rows, wave i takes the steps i, i + KS, ..., and their
 // sums are added in wave order through LDS, in fp32.  Gated, a wave has as many
 // gate as up rows, and a lane ends with both factors of an output.
+//
+// One row through 2048 x 2048 takes 3.2 us (1.4 of them a launch that does nothing),
+// through 11008 x 4096 6.7 us (3.6 TB/s); at 16 rows the rows of x, twice the weights'
+// bytes through LDS, count as well: gated 11008 x 4096 15.0 us (3.2 TB/s).
 #include <type_traits>
 
 #include "w4_launch.h"
