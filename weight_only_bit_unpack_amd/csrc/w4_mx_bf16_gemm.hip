@@ -15,7 +15,8 @@
 // MX block, 16 bytes with one scale.  Of a wave's 64 weight rows, tile j = 0, 1
 // takes rows 2 r + j (r the lane's column), so that a lane ends with neighbouring
 // outputs; gated, tile 0 takes gate rows and tile 1 the up rows beside them, so
-// that a lane ends with both factors.
+// that a lane ends with both factors, and of two rows one half of 32 lanes stores the
+// first and the other the second, neighbouring outputs a lane.
 //
 // Backward, the sum is over the rows of W, and its 4 bits lie along the other
 // index: a step's weights are rebuilt a step ahead, once for the block, to bf16
@@ -115,6 +116,10 @@ __device__ __forceinline__ int swizzle_r(int row, int c) {
   return c ^ (n1 << 3 | n0 << 2 | (n0 ^ c3) << 1 | (BN == 256 ? c4 : n1));
 }
 
+// Gated, lane r works on column gate_column(r) of a wave's 32: neighbours lie 16 lanes
+// apart.
+__device__ __forceinline__ int gate_column(int r) { return 2 * (r & 15) + (r >> 4); }
+
 template <int KIND, typename T>
 __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem P, GemmArgs G) {
   constexpr bool kBack = KIND == kMxBackward, kGate = KIND == kMxGated;
@@ -187,7 +192,7 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
   // forward: the weight row of LDS row i
   auto weight_row = [&](int i) -> int64_t {
     if constexpr (kGate) {
-      const int c = (i >> 6) * 32 + (i & 31);
+      const int c = (i >> 6) * 32 + gate_column(i & 31);
       return n0 + (c < cols_n ? c : cols_n - 1) + ((i >> 5) & 1) * P.n;
     } else {
       const int c = (i & ~63) + 2 * (i & 31) + ((i >> 5) & 1);
@@ -236,7 +241,7 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
 #pragma unroll
     for (int i = 0; i < T::IC; ++i) {
       const int row = ((waves * T::IC + i) * 64 + lane) / SC;
-      const int c = kGate ? (row >> 6) * 32 + (row & 31) : (row & ~63) + 2 * (row & 31) + ((row >> 5) & 1);
+      const int c = kGate ? (row >> 6) * 32 + gate_column(row & 31) : (row & ~63) + 2 * (row & 31) + ((row >> 5) & 1);
       cv[i] = (uint32_t)(c < cols_n ? c : cols_n - 1) * blocks + ((lane % SC) ^ swizzle_c(row));
     }
   }
@@ -609,15 +614,43 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
                                                 at + row_of(i, q) * pitch, 0, 0);
     }
   };
+  // Gated: rows q and q + 1 of a lane's column (v_permlane16_swap_b32) become the
+  // columns beside each other of row q in the first 16 lanes of 32, of q + 1 in the others.
+  // With lanes of the two rows by turns 4096 x 11008 x 4096 took 616 instead of 608 us
+  // (stores past the caches: gu the same, y 592, but the next product reads y).
+  auto put_gated = [&](void* base, int64_t out_pitch, int64_t col, bool bf16, auto&& value) {
+    const int size = bf16 ? 2 : 4;
+    const __amdgpu_buffer_rsrc_t d = resource(base, out_pitch, col, size);
+    const uint32_t pitch = (uint32_t)out_pitch * size;
+    if ((N & 1) == 0 && (reinterpret_cast<uintptr_t>(base) & 3) == 0) {
+      const int c = wn * 32 + 2 * (r & 15);
+      const uint32_t at = c < cols_n ? (uint32_t)(row0 + (r >> 4)) * pitch + (uint32_t)(size * c) : kStoreOOB;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int q = 0; q < 16; q += 2) {
+          const auto v = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, (float)value(i, q)),
+                                                          __builtin_bit_cast(uint32_t, (float)value(i, q + 1)), false, false);
+          const uint32_t even = v[0], odd = v[1];  // (a cast of the element itself takes the first one)
+          if (bf16)
+            __builtin_amdgcn_raw_buffer_store_b32(
+                cvt_pk_bf16(__builtin_bit_cast(float, even), __builtin_bit_cast(float, odd)), d,
+                at + row_of(i, q) * pitch, 0, 0);
+          else
+            __builtin_amdgcn_raw_buffer_store_b64((u32x2){even, odd}, d, at + row_of(i, q) * pitch, 0, 0);
+        }
+    } else if (bf16) {
+      put_bf16(d, pitch, wn * 32 + gate_column(r), false, value);
+    } else {
+      put_f32(d, pitch, wn * 32 + gate_column(r), value);
+    }
+  };
   if constexpr (kGate) {
-    const int c = wn * 32 + r;
     auto gate = [&](int i, int q) -> float { return acc[i][0][q]; };
     auto up = [&](int i, int q) -> float { return acc[i][1][q]; };
-    const bool even = (N & 1) == 0;
     if (P.gu) {
-      const bool pairs = even && (reinterpret_cast<uintptr_t>(P.gu) & 3) == 0;
-      put_bf16(resource(P.gu, 2 * N, n0, 2), (uint32_t)N * 4, c, pairs, gate);
-      put_bf16(resource(P.gu, 2 * N, N + n0, 2), (uint32_t)N * 4, c, pairs, up);
+      put_gated(P.gu, 2 * N, n0, true, gate);
+      put_gated(P.gu, 2 * N, N + n0, true, up);
     }
     with_activation(P.act, [&](auto ACT) {
 #pragma unroll
@@ -625,10 +658,7 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
 #pragma unroll
         for (int q = 0; q < 16; ++q) acc[i][0][q] = activate<decltype(ACT)::value>(acc[i][0][q]) * acc[i][1][q];
     });
-    if (P.y_bf16)
-      put_bf16(resource(P.y, N, n0, 2), (uint32_t)N * 2, c, even && (reinterpret_cast<uintptr_t>(P.y) & 3) == 0, gate);
-    else
-      put_f32(resource(P.y, N, n0, 4), (uint32_t)N * 4, c, gate);
+    put_gated(P.y, N, n0, P.y_bf16, gate);
   } else {
     const int size = P.y_bf16 ? 2 : 4;
     const __amdgpu_buffer_rsrc_t d = resource(P.y, N, n0, size);
