@@ -573,3 +573,93 @@ def test_binding_refusals(w4):
             w4.w4_mx_gated_linear_grad(b(4, 4), b(4, 8), wq, ws, act)
     with pytest.raises(w4.W4Error):                      # x from an odd element on
         w4.w4_mx_linear_bf16(b(4 * 64 + 1)[1:].view(4, 64), wq, ws)
+
+
+def test_activation_codes_that_are_none(w4):
+    report("mx_bf16_activation_codes")
+    u8 = lambda *s: torch.zeros(s, dtype=torch.uint8, device="cuda")
+    b = lambda *s: torch.zeros(s, dtype=BF16, device="cuda")
+    wq, ws = u8(8, 32), u8(8, 2)
+    for act, error in ((2 ** 32, w4.W4Error), (-2 ** 32 + 1, w4.W4Error), (2 ** 70, OverflowError),
+                       ("silu", TypeError), (None, TypeError)):
+        with pytest.raises(error):
+            w4.w4_mx_gated_linear(b(4, 64), wq, ws, act)
+        with pytest.raises(error):
+            w4.w4_mx_gated_linear_grad(b(4, 4), b(4, 8), wq, ws, act)
+
+
+# ------------------------------------------------------------------ shared memory
+@pytest.mark.parametrize("m,n,k", [(1, 64, 64), (40, 1000, 256), (40, 1002, 256), (70, 1001, 256), (5, 3, 64),
+                                   (300, 4104, 96)])
+def test_dgu_over_gu(w4, m, n, k):
+    """dgu may be gu's own memory."""
+    report("mx_bf16_dgu_over_gu", m=m, n=n, k=k)
+    g = np.random.default_rng(m + n)
+    wq, ws = weight(g, 2 * n, k)[:2]
+    dh, gu = dev(g.standard_normal((m, n))), dev(g.standard_normal((m, 2 * n)))
+    dx, dgu = w4.w4_mx_gated_linear_grad(dh, gu, wq, ws, w4.W4_GELU)
+    dx2, dgu2 = w4.w4_mx_gated_linear_grad(dh, gu, wq, ws, w4.W4_GELU, dgu=gu)
+    assert dgu2.data_ptr() == gu.data_ptr()
+    assert torch.equal(dgu, gu) and torch.equal(dx, dx2)
+
+
+def test_two_graphs_of_one_stream(w4):
+    """Two captured calls share their stream's workspace and counters; replayed by turns,
+    with eager work on other streams between, both stay right."""
+    report("mx_bf16_two_graphs")
+    g = np.random.default_rng(5)
+    side = torch.cuda.Stream()
+    sets = []
+    for m, n, k in ((40, 1001, 512), (96, 2048, 640)):
+        wq, ws, w = exact_weight(g, n, k)
+        sets.append([dev(exact_rows(g, m, n)), wq, ws, w])
+    torch.cuda.synchronize()
+    for dy, wq, ws, _ in sets:                            # makes the workspaces
+        w4.w4_mx_linear_grad(dy, wq, ws, dx_dtype=F32, stream=side)
+    torch.cuda.synchronize()
+    graphs = []
+    for dy, wq, ws, w in sets:
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph, stream=side):
+            dx = w4.w4_mx_linear_grad(dy, wq, ws, dx_dtype=F32)
+        graphs.append((graph, dx, dy, wq, ws, w))
+    for i in range(6):
+        for graph, dx, dy, wq, ws, w in graphs:
+            rows = exact_rows(g, *dy.shape)
+            dy.copy_(dev(rows))
+            graph.replay()
+            eager = w4.w4_mx_linear_grad(dy, wq, ws, dx_dtype=F32)
+            torch.cuda.synchronize()
+            same(dx, rows @ w)
+            same(eager, rows @ w)
+
+
+def test_two_threads(w4):
+    """Calls of two host threads, each on a stream of its own, while both make their
+    streams' first workspaces."""
+    report("mx_bf16_two_threads")
+    import threading
+    g = np.random.default_rng(6)
+    sets = []
+    for m, n, k in ((40, 1001, 512), (64, 700, 1024)):
+        wq, ws, w = exact_weight(g, n, k)
+        dy = exact_rows(g, m, n)
+        sets.append((dev(dy), wq, ws, dy @ w, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    outs = [[], []]
+
+    def work(i):
+        dy, wq, ws, _, stream = sets[i]
+        for _ in range(30):
+            outs[i].append(w4.w4_mx_linear_grad(dy, wq, ws, dx_dtype=F32, stream=stream))
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    for i, s in enumerate(sets):
+        assert len(outs[i]) == 30
+        for dx in outs[i]:
+            same(dx, s[3])

@@ -375,6 +375,12 @@ int64_t halves(int64_t rows) {
 const uint16_t* u16(const Tensor& t) { return static_cast<const uint16_t*>(t.const_data_ptr()); }
 uint16_t* u16(Tensor& t) { return static_cast<uint16_t*>(t.data_ptr()); }
 
+// an activation's code; what no int32 holds is none
+int32_t activation(PyObject* o) {
+  const long v = PyLong_AsLong(o);
+  return v == (int32_t)v ? (int32_t)v : -1;
+}
+
 // (x, wq, ws, y, y_dtype) -> y
 PyObject* linear_bf16(PyObject*, PyObject* const* a, Py_ssize_t n) {
   return guarded(n, 5, [&]() -> PyObject* {
@@ -399,7 +405,7 @@ PyObject* gated_linear(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const int64_t out = halves(rows);
     const Tensor& x = bf16_rows(a[0], "x", -1, k, dev);
     const int64_t m = x.size(0);
-    const long act = PyLong_AsLong(a[3]);
+    const int32_t act = activation(a[3]);
     Tensor gu;
     if (a[4] != Py_None) gu = bf16_rows(a[4], "gu", m, rows, dev);
     Tensor y = product_output(a[5], PyLong_AsLong(a[6]), m, out, x, dev);
@@ -434,7 +440,7 @@ PyObject* gated_linear_grad(PyObject*, PyObject* const* a, Py_ssize_t n) {
     const Tensor& dh = bf16_rows(a[0], "dh", -1, out, dev);
     const int64_t m = dh.size(0);
     const Tensor& gu = bf16_rows(a[1], "gu", m, rows, dev);
-    const long act = PyLong_AsLong(a[4]);
+    const int32_t act = activation(a[4]);
     Tensor dgu = a[5] == Py_None ? empty({m, rows}, at::kBFloat16, dh) : bf16_rows(a[5], "dgu", m, rows, dev);
     Tensor dx = product_output(a[6], PyLong_AsLong(a[7]), m, k, dh, dev, "dx");
     const w4_status st = w4_mx_gated_linear_grad(act, out, k, w, ws, u16(dh), u16(gu), m, u16(dgu), dx.data_ptr(),
