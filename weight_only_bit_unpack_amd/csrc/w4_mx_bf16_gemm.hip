@@ -23,7 +23,7 @@
 // rows in LDS, and ds_read_b64_tr_b16 gives a lane four rows of one column.
 //
 // Bound, many rows: by the card's power and the matrix cores, 61% busy with the clock down
-// to 1.6 to 1.9 GHz (gated 4096 x 11008 x 4096 616 us, 1.20 PFLOP/s; 2048 x 4096 x 11008 150
+// to 1.6 to 1.9 GHz (gated 4096 x 11008 x 4096 600 us, 1.23 PFLOP/s; 2048 x 4096 x 11008 150
 // us, 1.23; backward 4096 x 22016 x 4096 560 us, 1.32; the vendor library's dense product
 // of bf16 at 4096 x 22016 x 4096 624 us); few rows: by the chain of a step (0.4 to 0.8 us a
 // step of 64 whatever the tile below 128 x 256), the start and end of a launch and the
