@@ -177,8 +177,6 @@ int mx_bf16_skinny_shape(const MxBf16Problem& p);
 hipError_t launch_mx_bf16_skinny(const MxBf16Problem& p, int shape, hipStream_t stream);
 // few rows, backward (w4_mx_bf16_narrow.hip): `splits` blocks a tile, whose parts' sums
 // and counts (of each tile) are partial and counted
-int64_t mx_bf16_narrow_tiles(const MxBf16Problem& p);
-size_t mx_bf16_narrow_bytes(const MxBf16Problem& p, uint32_t splits);
 hipError_t launch_mx_bf16_narrow(const MxBf16Problem& p, uint32_t splits, char* partial, uint32_t* counted,
                                  hipStream_t stream);
 // For the tests, which name the kernel that they run: 16 * parts of the sum + tile

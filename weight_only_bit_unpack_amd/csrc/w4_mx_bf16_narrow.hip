@@ -199,17 +199,10 @@ __global__ __launch_bounds__(kThreads) void mx_bf16_narrow_kernel(MxBf16Problem 
 
 }  // namespace
 
-int64_t mx_bf16_narrow_tiles(const MxBf16Problem& p) {
-  return (p.m + kRows - 1) / kRows * ((p.k + kCols - 1) / kCols);
-}
-size_t mx_bf16_narrow_bytes(const MxBf16Problem& p, uint32_t splits) {
-  return splits == 1 ? 0 : (size_t)mx_bf16_narrow_tiles(p) * splits * kRows * kCols * sizeof(float);
-}
-
 hipError_t launch_mx_bf16_narrow(const MxBf16Problem& p, uint32_t splits, char* partial, uint32_t* counted,
                                  hipStream_t stream) {
-  const int64_t tiles = mx_bf16_narrow_tiles(p), tiles_m = (p.m + kRows - 1) / kRows;
-  const NarrowArgs g{(uint32_t)tiles_m, (uint32_t)(tiles / tiles_m), splits, reinterpret_cast<uint64_t*>(partial), counted};
+  const int64_t tiles_m = (p.m + kRows - 1) / kRows, tiles_n = (p.k + kCols - 1) / kCols, tiles = tiles_m * tiles_n;
+  const NarrowArgs g{(uint32_t)tiles_m, (uint32_t)tiles_n, splits, reinterpret_cast<uint64_t*>(partial), counted};
   const dim3 grid((uint32_t)((tiles * splits + 7) / 8 * 8));
   mx_bf16_narrow_kernel<<<grid, dim3(kThreads), 0, stream>>>(p, g);
   return hipGetLastError();
