@@ -588,10 +588,11 @@ w4_status w4_mx_grouped_linear(int32_t x_format, int32_t experts, int64_t n, int
  * few, their sums may be cut into at most 1024 parts in all, whose fp32 values (256 KB
  * of them at most a part) the last block of a tile adds in order; a backward product
  * whose summed length (n; gated 2 n) is not a multiple of 8 first copies its rows, 2
- * bytes a value, padded to one.  Both, and 8 KB of counters that every launch leaves at
+ * bytes a value, padded to one.  Both, and 30 KB of counters that every launch leaves at
  * zero, are kept per (device, stream) exactly as for w4_gemm (see there, also for
- * capture into a graph: one call of each shape on the capture stream before).  Forward
- * calls of at most 16 rows use none.
+ * capture into a graph: one call of each shape on the capture stream before; replays
+ * that overlap against what is said there spoil the overlapping calls' results only).
+ * Forward calls of at most 16 rows use none.
  */
 typedef enum {
   W4_SILU = 0,     /* g / (1 + e^-g) */

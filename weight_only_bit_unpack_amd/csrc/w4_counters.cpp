@@ -5,6 +5,13 @@
 // counters; calls on different streams never do, and hipStreamPerThread is a
 // stream of its own in each thread under one handle.  They are never freed, as
 // the workspaces (w4_workspace.cpp).
+//
+// Each number of parts has counters of its own.  A count goes round modulo the number
+// of parts, and a launch counts each of its tiles as often as that: so it is back at
+// zero when all launches have ended, in whatever order their blocks counted.  Were a
+// counter shared by launches of several numbers of parts, replays of captured calls
+// that overlap would leave counts behind, and every later sum in parts on the stream
+// would be joined too early.
 #include "w4_launch.h"
 
 #include <map>
@@ -13,7 +20,12 @@
 
 namespace w4 {
 
-hipError_t stream_counters(hipStream_t stream, uint32_t** out) {
+namespace {
+constexpr int kSet = kMxMaxParts / 2, kCounters = (kMxMaxSplits - 1) * kSet;  // of a number of parts, all
+}  // namespace
+
+hipError_t stream_counters(hipStream_t stream, uint32_t splits, uint32_t** out) {
+  if (splits < 2 || splits > (uint32_t)kMxMaxSplits) return hipErrorInvalidValue;
   static std::mutex mu;
   static std::map<std::tuple<int, hipStream_t, uint64_t>, uint32_t*> kept;
   int dev = 0;
@@ -29,16 +41,16 @@ hipError_t stream_counters(hipStream_t stream, uint32_t** out) {
     if (e != hipSuccess) return e;
     if (capture != hipStreamCaptureStatusNone) return hipErrorStreamCaptureUnsupported;
     uint32_t* p = nullptr;
-    e = hipMalloc(reinterpret_cast<void**>(&p), kMxCounters * sizeof(uint32_t));
+    e = hipMalloc(reinterpret_cast<void**>(&p), kCounters * sizeof(uint32_t));
     if (e != hipSuccess) return e;
-    e = launch_zero(p, kMxCounters, 0, stream);
+    e = launch_zero(p, kCounters, 0, stream);
     if (e != hipSuccess) {
       (void)hipFree(p);  // (nothing uses it yet)
       return e;
     }
     slot = p;
   }
-  *out = slot;
+  *out = slot + (splits - 2) * kSet;
   return hipSuccess;
 }
 

@@ -85,10 +85,14 @@ hipError_t stream_workspace(int user, hipStream_t stream, size_t bytes, char** o
 // A number of the calling thread from 1 on, never given again (the system gives
 // an ended thread's id again, while its last kernels may still run).
 uint64_t this_thread();
-// kMxCounters counters of (current device, stream), zeros to begin with: every
-// kernel that counts in them leaves zeros behind (w4_counters.cpp).
-constexpr int kMxCounters = 2048;
-hipError_t stream_counters(hipStream_t stream, uint32_t** out);
+// A product's sums may be cut into kMxMaxParts parts in all, a tile's into kMxMaxSplits
+// (256 MB of sums on the largest tile; more than four blocks a CU are not worth their
+// joining).
+constexpr int kMxMaxParts = 1024, kMxMaxSplits = 16;
+// A counter for each tile that a launch cuts into `splits` parts (2 .. kMxMaxSplits; at
+// most kMxMaxParts / splits tiles), of (current device, stream), zeros to begin with:
+// every launch that counts in them leaves zeros behind (w4_counters.cpp).
+hipError_t stream_counters(hipStream_t stream, uint32_t splits, uint32_t** out);
 
 // ws: a workspace of at least gemm_workspace_bytes(...) bytes, or nullptr for
 // the library-kept one of the stream (stream_workspace)

@@ -82,7 +82,7 @@ using T3 = Tile<64, 128, 2, 2, 2, 3, 2, 2>;
 using T4 = Tile<32, 64, 1, 1, 4, 3, 2>;  // (backward: the narrow kernel, whose tiles are the same)
 constexpr int kTiles = 5;
 
-constexpr uint32_t kMaxSplits = 16;
+constexpr uint32_t kMaxSplits = kMxMaxSplits;
 // An offset past the resource of a tile's outputs (below 2^31 bytes), also with
 // the offset of a row added.
 constexpr uint32_t kStoreOOB = 0x80000000u;
@@ -734,10 +734,7 @@ struct Plan {
 int64_t outputs(const MxBf16Problem& p) { return p.kind == kMxBackward ? p.k : p.n; }
 int64_t steps_of(const MxBf16Problem& p) { return ((p.kind == kMxBackward ? p.n : p.k) + 63) / 64; }
 
-// Tiles that are cut at most (their counts have a place each), and parts that they are
-// cut into at most (256 MB of sums on the largest tile; more than four blocks a CU are
-// not worth their joining).
-constexpr int64_t kMaxCut = kMxCounters, kMaxParts = 1024;
+constexpr int64_t kMaxParts = kMxMaxParts;
 
 // Tile number t, the tiles from `whole` on in s parts (s == 1: none); tile < 0
 // where they do not fit the problem: a tile's rows of x and of outputs stay below
@@ -751,7 +748,7 @@ Plan plan_on(const MxBf16Problem& p, int t, uint32_t s, int64_t whole) {
   if (s == 1) q.whole = tiles;
   constexpr int64_t kTileBytes = (INT64_C(1) << 31) - 1;
   if (4 * wide > kTileBytes / T::BM || 2 * p.x_pitch > kTileBytes / T::BM) q.tile = -1;
-  if (q.whole > tiles || (int64_t)s > steps_of(p) || (s > 1 && (q.cut() > kMaxCut || q.cut() * s > kMaxParts))) q.tile = -1;
+  if (q.whole > tiles || (int64_t)s > steps_of(p) || (s > 1 && q.cut() * s > kMaxParts)) q.tile = -1;
   if (std::is_same_v<T, T4> && p.kind == kMxBackward && s > 1 && q.whole > 0) q.tile = -1;  // (all tiles or none)
   if ((tiles + kMaxParts + 14) * T::THREADS > kMaxLaunchThreads) q.tile = -1;
   return q;
@@ -863,7 +860,7 @@ hipError_t launch_plan(const MxBf16Problem& problem, const Plan& q, size_t reser
     const size_t bytes = reserve + (q.splits > 1 ? (size_t)q.cut() * q.splits * T::BM * T::BN * sizeof(float) : 0);
     char* ws = nullptr;
     hipError_t e = bytes ? stream_workspace(kWorkspaceMx, stream, bytes, &ws) : hipSuccess;
-    if (e == hipSuccess && q.splits > 1) e = stream_counters(stream, &g.counted);
+    if (e == hipSuccess && q.splits > 1) e = stream_counters(stream, q.splits, &g.counted);
     if (e == hipSuccess) e = fill(p, ws);
     if (e != hipSuccess) return e;
     g.partial = reinterpret_cast<uint64_t*>(ws + reserve);
