@@ -28,6 +28,8 @@
  *    hipStreamPerThread: per thread) for the process's life (see there).
  *  - `stream` is a hipStream_t (NULL = the null stream).  A call only enqueues
  *    work on it; it never synchronises the stream or the device.
+ *  - Several host threads may call at once, on one stream too: the launches of a
+ *    call that uses a workspace have none of another call's on it between them.
  *  - All validation happens on the host before anything is enqueued.  On any
  *    error return nothing is enqueued and no output byte changes.  Faults in
  *    the kernels surface at the caller's next synchronisation.

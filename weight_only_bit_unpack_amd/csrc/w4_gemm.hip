@@ -641,6 +641,7 @@ hipError_t launch_gemm_shape(int codec, const GemvProblem& p, int m, int y_bf16,
   const uint32_t tiles_m = g.tiles_m, tiles = g.tiles;
   if (too_large(g.pack_blocks, 256) || too_large((int64_t)g.tiles_m * g.tiles_n * S, 512)) return kTooLarge;
   const size_t xpk_bytes = g.xpk_bytes, per_split = g.per_split;
+  const auto turn = stream_turn(stream);
   hipError_t e = hipSuccess;
   if (!ws) {
     e = stream_workspace(kWorkspaceGemm, stream, g.bytes, &ws);

@@ -744,7 +744,9 @@ hipError_t launch_one(const GemvProblem& p, int m, int y_bf16, const GemvShape& 
   const int64_t blocks = (p.n + rows - 1) / rows;
   if (too_large(blocks, 64 * WAVES)) return kTooLarge;
   Slicing sl{sh.kslices, sh.slice_steps, nullptr};
+  std::unique_lock<std::mutex> turn;
   if (sh.kslices > 1) {
+    turn = stream_turn(stream);
     char* ws = nullptr;
     const hipError_t e =
         stream_workspace(kWorkspaceGemv, stream, (size_t)sh.kslices * m * p.n * 4, &ws);

@@ -6,6 +6,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+#include <mutex>
+
 namespace w4 {
 
 // A launch holds fewer than 2^32 threads (HIP cuts a larger one without an error).
@@ -82,6 +84,11 @@ hipError_t launch_gemv_batched(int codec, const GemvProblem* probs_dev, int coun
 // use it), so it never waits for the stream.
 enum { kWorkspaceGemm = 0, kWorkspaceGemv = 1, kWorkspaceMx = 2 };
 hipError_t stream_workspace(int user, hipStream_t stream, size_t bytes, char** out);
+// The calling thread's turn on a stream (of the current device).  A call that fills a
+// workspace in one launch and reads it in a later one holds it from the lookup of the
+// workspace to its last launch, so that another host thread's call on the stream comes
+// before or behind all of them.  Streams' turns are apart.
+[[nodiscard]] std::unique_lock<std::mutex> stream_turn(hipStream_t stream);
 // A number of the calling thread from 1 on, never given again (the system gives
 // an ended thread's id again, while its last kernels may still run).
 uint64_t this_thread();

@@ -859,6 +859,8 @@ hipError_t launch_plan(const MxBf16Problem& problem, const Plan& q, size_t reser
     using T = decltype(X);
     const size_t bytes = reserve + (q.splits > 1 ? (size_t)q.cut() * q.splits * T::BM * T::BN * sizeof(float) : 0);
     char* ws = nullptr;
+    std::unique_lock<std::mutex> turn;  // (parts are put and added in one launch)
+    if (reserve > 0) turn = stream_turn(stream);
     hipError_t e = bytes ? stream_workspace(kWorkspaceMx, stream, bytes, &ws) : hipSuccess;
     if (e == hipSuccess && q.splits > 1) e = stream_counters(stream, q.splits, &g.counted);
     if (e == hipSuccess) e = fill(p, ws);

@@ -685,7 +685,9 @@ hipError_t launch_tile(const MxProblem& p, const GemmArgs& g, uint32_t blocks, h
 template <int AF>
 hipError_t launch_gemm_format(const MxProblem& p, const Plan& q, hipStream_t stream) {
   GemmArgs g{(uint32_t)q.tiles_m, (uint32_t)q.tiles_n, q.splits, nullptr};
+  std::unique_lock<std::mutex> turn;
   if (q.splits > 1) {
+    turn = stream_turn(stream);
     char* ws = nullptr;
     const hipError_t e =
         stream_workspace(kWorkspaceMx, stream, (size_t)q.splits * p.m * p.n * sizeof(float), &ws);
