@@ -83,7 +83,8 @@ typedef enum {
                           weight, a GEMM with 2^35 values of x or 2^38 of Y)            */
   W4_EALIGN = 3,       /* a pointer not aligned as the call states                      */
   W4_EUNSUPPORTED = 4, /* a codec / dtype combination the call does not provide         */
-  W4_EHIP = 5          /* the kernel launch failed (hipGetLastError)                    */
+  W4_EHIP = 5          /* the kernel launch failed (hipGetLastError), or memory for
+                          a workspace or a plan, the host's too, ran out                */
 } w4_status;
 
 /* W4_LUT16S: the LUT16 rebuild with one 16-level table for the whole weight

@@ -13,7 +13,7 @@ HERE = os.path.join(ROOT, "tests", "launches")
 
 @pytest.mark.skipif(shutil.which("g++") is None or not os.path.isdir("/opt/rocm/include"),
                     reason="needs g++ and the HIP headers")
-@pytest.mark.parametrize("check", ["counters_check", "turns_check"])
+@pytest.mark.parametrize("check", ["counters_check", "turns_check", "throws_check"])
 def test_launches(tmp_path, check):
     import weight_only_bit_unpack_amd as w4
     exe = str(tmp_path / check)

@@ -219,8 +219,10 @@ w4_status w4_gemv(int32_t codec, int64_t n, int64_t k, const uint8_t* packed,
   if (k == 0)  // the empty sum
     return launched(w4::launch_zero(y, (int64_t)m * n, y_dtype == W4_BF16,
                                     static_cast<hipStream_t>(stream)));
-  return launched(w4::launch_gemv(codec, problem(n, k, packed, scales, codebook, x, y), m,
-                                  y_dtype == W4_BF16, static_cast<hipStream_t>(stream)));
+  return launched(w4::caught([&] {
+    return w4::launch_gemv(codec, problem(n, k, packed, scales, codebook, x, y), m,
+                           y_dtype == W4_BF16, static_cast<hipStream_t>(stream));
+  }));
 }
 
 w4_status w4_gemm(int32_t codec, int64_t n, int64_t k, const uint8_t* packed,
@@ -233,8 +235,10 @@ w4_status w4_gemm(int32_t codec, int64_t n, int64_t k, const uint8_t* packed,
   if (k == 0)  // the empty sum
     return launched(w4::launch_zero(y, (int64_t)m * n, y_dtype == W4_BF16,
                                     static_cast<hipStream_t>(stream)));
-  return launched(w4::launch_gemm(storage_codec(codec), problem(n, k, packed, scales, codebook, x, y),
-                                  m, y_dtype == W4_BF16, static_cast<hipStream_t>(stream), nullptr));
+  return launched(w4::caught([&] {
+    return w4::launch_gemm(storage_codec(codec), problem(n, k, packed, scales, codebook, x, y),
+                           m, y_dtype == W4_BF16, static_cast<hipStream_t>(stream), nullptr);
+  }));
 }
 
 w4_status w4_gemm_noalloc(int32_t codec, int64_t n, int64_t k, const uint8_t* packed,
@@ -250,9 +254,11 @@ w4_status w4_gemm_noalloc(int32_t codec, int64_t n, int64_t k, const uint8_t* pa
   codec = storage_codec(codec);
   if (w4::gemm_workspace_bytes(codec, n, k, m) > w4::kNoallocScratchBytes) return W4_ESHAPE;
   char* ws = nullptr;
-  if (w4::noalloc_scratch(&ws) != hipSuccess) return W4_EHIP;
-  return launched(w4::launch_gemm(codec, problem(n, k, packed, scales, codebook, x, y), m,
-                                  y_dtype == W4_BF16, static_cast<hipStream_t>(stream), ws));
+  if (w4::caught([&] { return w4::noalloc_scratch(&ws); }) != hipSuccess) return W4_EHIP;
+  return launched(w4::caught([&] {
+    return w4::launch_gemm(codec, problem(n, k, packed, scales, codebook, x, y), m,
+                           y_dtype == W4_BF16, static_cast<hipStream_t>(stream), ws);
+  }));
 }
 
 w4_status w4_linear(int32_t codec, int64_t n, int64_t k, const uint8_t* packed,
@@ -294,7 +300,12 @@ w4_status w4_gemv_batched_plan(int32_t codec, int32_t m, int32_t y_dtype,
   if (w4::too_large(total, 256)) return W4_ESHAPE;
   // Work is handed out in tile order; giving the longest rows (largest k) the
   // first tiles leaves short tiles for the end of the launch.
-  std::vector<int32_t> order((size_t)count);
+  std::vector<int32_t> order;
+  const hipError_t e = w4::caught([&] {
+    order.resize((size_t)count);
+    return hipSuccess;
+  });
+  if (e != hipSuccess) return W4_EHIP;
   for (int32_t i = 0; i < count; ++i) order[(size_t)i] = i;
   std::stable_sort(order.begin(), order.end(),
                    [&](int32_t a, int32_t b) { return problems[a].k > problems[b].k; });

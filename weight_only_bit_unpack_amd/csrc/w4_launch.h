@@ -16,6 +16,17 @@ constexpr int64_t kMaxLaunchThreads = 0xFFFFFFFF;
 constexpr hipError_t kTooLarge = hipErrorInvalidConfiguration;
 inline bool too_large(int64_t blocks, int threads) { return blocks > kMaxLaunchThreads / threads; }
 
+// f()'s error.  A launcher may allocate on the host (the tables of workspaces); nothing
+// that it throws passes the C boundary.
+template <typename F>
+hipError_t caught(F&& f) {
+  try {
+    return f();
+  } catch (...) {
+    return hipErrorOutOfMemory;
+  }
+}
+
 // f(first, count) over parts of at most `most` of `total`, until one fails: the
 // launches of an elementwise call.
 template <typename F>

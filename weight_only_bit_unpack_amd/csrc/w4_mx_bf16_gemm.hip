@@ -922,7 +922,9 @@ extern "C" int32_t w4_mx_bf16_product_on(int32_t kernel, int32_t kind, int32_t a
     return plan_on<decltype(X)>(p, tile, (uint32_t)parts, tiles > cus ? tiles / cus * cus : tiles / 2 / 8 * 8);
   });
   if (q.tile < 0) return hipErrorInvalidValue;
-  return launch_plan(p, q, 0, static_cast<hipStream_t>(stream), [](MxBf16Problem&, char*) { return hipSuccess; });
+  return caught([&] {
+    return launch_plan(p, q, 0, static_cast<hipStream_t>(stream), [](MxBf16Problem&, char*) { return hipSuccess; });
+  });
 }
 
 }  // namespace w4

@@ -5,6 +5,7 @@
 #include <stdint.h>
 
 #include "w4.h"
+#include "w4_launch.h"
 
 namespace w4 {
 
@@ -12,15 +13,9 @@ inline bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintp
 
 inline w4_status launched(hipError_t e) { return e == hipSuccess ? W4_OK : W4_EHIP; }
 
-// The launchers may allocate a workspace or grow a table of them; nothing they
-// throw passes the C boundary.
 template <typename F>
 w4_status guarded(F&& f) {
-  try {
-    return launched(f());
-  } catch (...) {
-    return W4_EHIP;
-  }
+  return launched(caught(f));
 }
 
 inline w4_status check_y(const void* y, int32_t y_dtype) {

@@ -750,7 +750,8 @@ extern "C" int32_t w4_mx_product_on(int32_t kernel, int32_t x_fmt, int32_t exper
     const Plan q = with_tile<decltype(AF)::value>(kernel % 16, [&](auto X) {
       return plan_on<decltype(X)>(p, kernel % 16, parts);
     });
-    return q.tile < 0 ? hipErrorInvalidValue : launch_gemm_format<decltype(AF)::value>(p, q, on);
+    if (q.tile < 0) return hipErrorInvalidValue;
+    return caught([&] { return launch_gemm_format<decltype(AF)::value>(p, q, on); });
   };
   return x_fmt == kMxFp8 ? go(std::integral_constant<int, kMxFp8>{}) : go(std::integral_constant<int, kMxFp4>{});
 }
