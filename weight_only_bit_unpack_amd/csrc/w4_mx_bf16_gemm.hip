@@ -79,7 +79,7 @@ using T0 = Tile<256, 256, 2, 4, 1, 3, 2>;
 using T1 = Tile<128, 256, 2, 4, 1, 3, 3, 4>;
 using T2 = Tile<128, 128, 2, 2, 1, 3, 2>;
 using T3 = Tile<64, 128, 2, 2, 2, 3, 2, 2>;
-using T4 = Tile<32, 64, 1, 1, 4, 3, 2>;  // (backward: the narrow kernel, whose tiles are the same)
+using T4 = Tile<32, 64, 1, 1, 4, 3, 0>;  // (backward: the narrow kernel, whose tiles are the same)
 constexpr int kTiles = 5;
 
 constexpr uint32_t kMaxSplits = kMxMaxSplits;
@@ -371,19 +371,19 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
     }
   };
   // ---- backward: the weights of step n, in ring slot s, rebuilt to rows of bf16.
-  // A wave takes the units that it copied itself: 32 values of one row and block.
+  // A wave takes the unit a lane that it copied itself: 32 values of one row and block.
   struct Unit {
     u32x4 w;
     uint32_t s;
   };
-  auto read_unit = [&](Unit& v, uint32_t s, int i) {
-    const int u = (wave * T::IW + i) * 64 + lane;
+  auto read_unit = [&](Unit& v, uint32_t s) {
+    const int u = wave * 64 + lane;
     v.w = lds[slot_w(s) + u];
     v.s = reinterpret_cast<const uint32_t*>(lds + slot_s(s))[u];
   };
-  auto rebuild_unit = [&](const Unit& v, uint32_t n, int i) {
+  auto rebuild_unit = [&](const Unit& v, uint32_t n) {
     if constexpr (kBack) {
-      const int u = (wave * T::IW + i) * 64 + lane, row = u / U, c = u % U;
+      const int u = wave * 64 + lane, row = u / U, c = u % U;
 #pragma unroll
       for (int e = 0; e < 4; ++e)
         lds[slot_r(n) + row * (T::BN / 8) + swizzle_r<T::BN>(row, 4 * c + e)] = mx_rebuild8(v.w[e], v.s);
@@ -419,11 +419,11 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
   using Q3 = std::integral_constant<int, 3>;
 
   // ---- the loop.  A quarter's operands are read and rebuilt while the one before
-  // is multiplied, backward the next step's weights too, a unit a quarter.  The
+  // is multiplied, backward the next step's weights too, in the first quarter.  The
   // barrier of a step comes before its last quarter: by then every wave holds that
   // in registers, so the step's slot can take the copies of step t + NS, and the
   // next step's first operands are read, while it is multiplied.
-  static_assert(T::IW <= 2, "a unit in each of the first two quarters");
+  static_assert(!kBack || T::IW == 1, "a wave rebuilds one unit a lane");
   Step st;
   Quarter o0, o1;
   Weights b0, b1;
@@ -432,20 +432,16 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
   auto step = [&](uint32_t n, auto FAST) {
     constexpr bool fast = decltype(FAST)::value;  // step n + NS exists and is whole
     const uint32_t next = cur + 1 == NS ? 0 : cur + 1;
-    if constexpr (kBack) read_unit(unit, next, 0);
+    if constexpr (kBack) read_unit(unit, next);
     read(o1, cur, Q1{});
     weights(b1, st, n, Q1{});
     multiply(o0, b0);
     interleave();
-    if constexpr (kBack) {
-      rebuild_unit(unit, n + 1, 0);
-      if constexpr (T::IW > 1) read_unit(unit, next, 1);
-    }
+    if constexpr (kBack) rebuild_unit(unit, n + 1);
     read(o0, cur, Q2{});
     weights(b0, st, n, Q2{});
     multiply(o1, b1);
     interleave();
-    if constexpr (kBack && T::IW > 1) rebuild_unit(unit, n + 1, 1);
     read(o1, cur, Q3{});
     weights(b1, st, n, Q3{});
     multiply(o0, b0);
@@ -490,11 +486,8 @@ __global__ __launch_bounds__(T::THREADS) void mx_bf16_gemm_kernel(MxBf16Problem 
       else
         __builtin_amdgcn_s_waitcnt(wait_vm(0));
       lds_barrier();
-#pragma unroll
-      for (int j = 0; j < T::IW; ++j) {
-        read_unit(unit, 0, j);
-        rebuild_unit(unit, 0, j);
-      }
+      read_unit(unit, 0);
+      rebuild_unit(unit, 0);
       __builtin_amdgcn_s_waitcnt(kWaitLds);
       lds_barrier();
     }
