@@ -752,14 +752,17 @@ Plan plan_on(const MxBf16Problem& p, int t, uint32_t s, int64_t whole) {
 // fit) first2 + step2; but a step of all blocks together no less than its operations
 // at `rate` (PFLOP/s, tile 0 and the others), which is what the card's power allows.
 // A launch takes `launch`, and sums in parts take `join` and, for each part, `part` and
-// its bytes at 64 KB a `copy`.  Fitted to 8900 times of every tile and number of parts
-// over 17 to 8192 rows, 300 to 22016 columns and sums of 300 to 22016 (root mean square of
-// the error 7.5 to 8%); the plans they choose take 0.7 to 1.4% more than the best ones on
-// average.  Examples (us, graph replays): 64 x 1000 x 4096 8.6 on tile 4 in four parts,
-// 10.7 in one, 11.7 on tile 3 in four; gated 333 x 2730 x 2080 21.0 on tile 2, 22.1 on
-// tile 3 and 19.4 there with the last round's tiles in three parts, 24.2 on tile 4; 2048 x
-// 4096 x 11008 150 on tile 1, 158 on tile 0 in two parts, 192 in one; backward 165 on
-// tile 0 with the last round's tiles in two parts, 185 without, 198 on tile 1.
+// its bytes at 64 KB a `copy`.  perf/mx_bf16_plans.py times every tile and number of parts
+// and fits these; the table in profiles/mx_bf16_plans.txt holds 8735 times of 447 products of
+// 1 to 8192 rows, 300 to 22016 columns and sums of 300 to 22016, on which their error is 7.7
+// to 8.0% (root mean square).  The plans they choose take 0.8% more there than the best ones
+// on average, and at most 1.22 times as long (333 x 5500 x 4096, 30.5 us in three parts on
+// tile 1, 24.9 on tile 3 with the last round's tiles in four): plans beside each other differ
+// by less than the error.  Examples (us, graph replays): 64 x 1000 x 4096 8.5 on tile 4 in
+// four parts, 10.7 in one, 11.6 on tile 3 in four; gated 333 x 2730 x 2080 21.1 on tile 2,
+// 21.7 on tile 3 and 19.2 there with the last round's tiles in three parts, 23.5 on tile 4;
+// 2048 x 4096 x 11008 148 on tile 1, 155 on tile 0 in two parts, 192 in one; backward 163 on
+// tile 0 with the last round's tiles in two parts, 184 without, 191 on tile 1.
 struct Cost {
   float first, step, first2, step2;  // first2 == 0: one block a CU
 };
