@@ -12,7 +12,8 @@
 // The weight's 4 bits lie along the columns, the sum goes over its rows: the 64 rows of
 // a step are rebuilt to bf16 by the lanes that loaded them into 8 KB of the wave's own
 // LDS, and ds_read_b64_tr_b16 gives a lane four rows of one column.  A wave's LDS
-// accesses are carried out in order, so nothing waits in between.
+// accesses are carried out in order, so nothing waits in between; a step's rows are
+// rebuilt behind the last step's reads, since they share the area.
 #include "w4_launch.h"
 #include "w4_mx_device.h"
 #include "w4_mx_parts.h"
